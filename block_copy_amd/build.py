@@ -27,8 +27,9 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 ARCH = "gfx950"
 
-HOST_SOURCES = ["plan.cpp", "runtime.cpp", "jobs.cpp", "autotune.cpp"]
-HIP_SOURCES = ["kvcopy_kernel.hip", "device_batch.hip", "order_kernel.hip"]
+HOST_SOURCES = ["plan.cpp", "runtime.cpp", "jobs.cpp", "autotune.cpp", "cache.cpp"]
+HIP_SOURCES = ["kvcopy_kernel.hip", "device_batch.hip", "order_kernel.hip", "cache_kernels.hip",
+               "attention.hip"]
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall",
     # Keep the compiler away from packed fp32 instructions on this target.

@@ -1,0 +1,924 @@
+// attention.hip -- attention of new tokens over the paged cache.
+//
+//   out = sum_j p_j v_j / sum_j p_j,   p_j = exp2(c q . k_j - m),   c = scale * log2(e)
+//
+// in one pass over the keys: a running maximum m and sum of each row, and the
+// rows of the output rescaled when m has grown by more than 2^kSlack.
+//
+// Rows.  The query heads of one key/value head see the same keys, so a row is
+// a (token, query head) pair, r = token * group + head: a tile of rows reads
+// each key once for all of them, and a decode step's single token still fills
+// `group` columns of a matrix instruction.
+//
+// Products.  Both are transposed: S' = K Q' has one query row to a column, so
+// a lane holds several keys' scores of one row; their maximum needs one or two
+// exchanges between lanes, and the weights are already where the second
+// product, O' = V' P', takes its right operand, up to an order of the keys
+// that V' is read in as well.  V' comes out of row-major shared memory through
+// the transposing read (ds_read_b64_tr_b16: of a 4 x 16 block whose row i is
+// given by lanes 4 i .. 4 i + 3 of sixteen, lane j gets column j).
+//
+// c > 0: the sign of a negative scale goes into q, and a scale of 0 is a q of 0.
+//
+// What a row does not see is not read, or its score is set to -infinity; a
+// value row that some rows of a tile see and others do not is multiplied by an
+// exact 0 for the latter, except that 0 * infinity is NaN: tiles at the mask's
+// edge look for such values and take the long way (`hidden_product`).
+#include <hip/hip_runtime.h>
+
+#include "cache_internal.h"
+#include "cache_types.h"
+
+namespace kvc {
+namespace {
+
+constexpr float kSlack = 8.0f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr int kTileWaves = 4;     // wavefronts of a tile kernel's workgroup, 32 rows each
+constexpr int kTileRows = 32 * kTileWaves;
+constexpr int kSingleWaves = 4;   // of the kernel for few rows: each its own keys
+constexpr int kSingleRows = 16;
+constexpr int kSingleKeys = 32;   // keys of a wavefront's step
+
+typedef int16_t i16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+
+// A format's rows as the matrix instructions take them.  V: the type of the
+// second product.  8-bit codes become bf16 there whatever the queries' type,
+// since a weight times a value's scale may leave fp16's range.
+template <class T, class F>
+struct Held {
+    static constexpr bool coded = true;
+    typedef u32x2 piece;   // 8 codes
+    typedef Bf16 V;
+    static __device__ __forceinline__ u32x4 key(piece p) { return Widen<T, F>::eight(p); }
+    static __device__ __forceinline__ u32x4 value(piece p) { return Widen<Bf16, F>::eight(p); }
+};
+template <class T>
+struct Held<T, void> {
+    static constexpr bool coded = false;
+    typedef u32x4 piece;   // 8 values
+    typedef T V;
+    static __device__ __forceinline__ u32x4 key(piece p) { return p; }
+    static __device__ __forceinline__ u32x4 value(piece p) { return p; }
+};
+
+// Lanes 0-31 and 32-63 exchange.
+__device__ __forceinline__ float other_half(float x)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float((threadIdx.x & 32u) ? r[0] : r[1]);
+}
+
+// Eight values of one column, keys `first` .. + 3 and `second` .. + 3 of the
+// lane's group of sixteen, from row-major shared memory: `at` is this lane's
+// address for row first + (lane % 16) / 4 and columns 4 (lane % 4) .. + 3.
+__device__ __forceinline__ u32x4 columns(const uint8_t *at, int second)
+{
+    const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)at));
+    const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(at + second)));
+    return u32x4{a.x, a.y, b.x, b.y};
+}
+
+// Whether any of eight 16-bit values is an infinity or a NaN.
+template <class T>
+__device__ __forceinline__ bool any_special(u32x4 p)
+{
+    bool r = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        r |= (p[i] & T::kExponent) == T::kExponent || (p[i] >> 16 & T::kExponent) == T::kExponent;
+    return r;
+}
+
+// Eight values with infinities and NaN taken out (`clean`), and marks in their
+// place: 1 for +infinity, 1/256 for -infinity, 256 for NaN.  A sum of up to 64
+// marks says which of them there were.
+template <class T>
+__device__ __forceinline__ void part_special(u32x4 p, u32x4 &clean, u32x4 &marks)
+{
+    float m[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t h = p[i / 2] >> (16 * (i % 2)) & 0xffffu;
+        const bool special = (h & T::kExponent) == T::kExponent;
+        const bool nan = special && (h & ((T::kExponent & (0u - T::kExponent)) - 1));
+        m[i] = !special ? 0.0f : nan ? 256.0f : h & 0x8000u ? 1.0f / 256 : 1.0f;
+        if (special)
+            p[i / 2] &= i % 2 ? 0x0000ffffu : 0xffff0000u;
+    }
+    clean = p;
+    marks = pack8<T>(m);
+}
+__device__ __forceinline__ float special_of(float marks)
+{
+    const float nan = __builtin_floorf(marks * (1.0f / 256));
+    marks -= nan * 256.0f;
+    const float up = __builtin_floorf(marks);
+    const bool down = marks - up > 0.0f;
+    if (nan > 0.0f || (up > 0.0f && down))
+        return __builtin_nanf("");
+    return up > 0.0f ? __builtin_inff() : down ? -__builtin_inff() : 0.0f;
+}
+
+// The sequence of this workgroup: its query rows and keys, bounded by what the
+// host said, so that no value in q_starts or context_lens leads outside.
+struct Sequence {
+    int32_t q0, n, ctx, bound;   // first token, tokens, context, tokens that may be looked up
+};
+__device__ __forceinline__ Sequence sequence_of(const AttentionArgs &a, uint32_t s)
+{
+    Sequence r;
+    const int32_t first = a.q_starts[s], end = a.q_starts[s + 1], total = (int32_t)a.total_q;
+    r.q0 = first < 0 ? 0 : first < total ? first : total;
+    const int32_t q1 = end < r.q0 ? r.q0 : end < total ? end : total;
+    r.n = q1 - r.q0;
+    r.ctx = a.context_lens[s];
+    bool bad = first != r.q0 || end != q1 || r.ctx < 0;
+    if (r.ctx < 0)
+        r.ctx = 0;
+    r.bound = r.ctx < (int32_t)a.max_context ? r.ctx : (int32_t)a.max_context;
+    bad |= r.ctx != r.bound;
+    if (r.n > (int32_t)a.max_q_len)
+        bad = true;
+    if (bad && threadIdx.x == 0)
+        set_status(a.status, KVCACHE_BAD_LENGTH);
+    return r;
+}
+
+// The page and place of token t, or a page of ~0 for one that reads as zeros.
+struct Place {
+    uint32_t page, place;
+};
+__device__ __forceinline__ Place place_of(const AttentionArgs &a, const int32_t *table, int32_t t, int32_t end)
+{
+    Place p;
+    p.page = ~0u;
+    p.place = 0;
+    if (t < end) {
+        const uint32_t column = a.page_size.div((uint32_t)t);
+        p.place = a.page_size.mod((uint32_t)t, column);
+        p.page = (uint32_t)table[column];
+        if (p.page >= a.num_pages) {
+            set_status(a.status, KVCACHE_BAD_PAGE);
+            p.page = ~0u;
+        }
+    }
+    return p;
+}
+
+// Where row r's results go; used by both kernels.
+template <class T>
+__device__ __forceinline__ void store4(typename T::elem *out, const float *x)
+{
+    u32x2 w;
+    w.x = pack2<T>(x[0], x[1]);
+    w.y = pack2<T>(x[2], x[3]);
+    *(u32x2 *)out = w;
+}
+
+// ---- many rows --------------------------------------------------------------
+//
+// A workgroup of 4 wavefronts takes 128 rows of one (sequence, key/value head)
+// and walks the keys in tiles of Keys, all wavefronts reading the same tile
+// from shared memory.  The next tile's rows are in flight to registers while a
+// tile is worked on, and go to the other shared buffer at its end: one barrier
+// a tile.  Rows of shared memory are padded so that neither the 16-byte reads
+// of K (stride = 16 bytes mod 256) nor the transposing reads of V (64 mod 256)
+// meet in a bank.
+
+template <int DP>
+struct TileShape {
+    static constexpr int kKeys = DP <= 128 ? 64 : 32;
+    static constexpr int kKStride = DP * 2 + 16;
+    static constexpr int kVStride = DP * 2 + 64;
+    static constexpr int kKBytes = kKeys * kKStride;
+    static constexpr int kVBytes = kKeys * kVStride;
+    static constexpr int kScaleBytes = kKeys * 8;
+    static constexpr int kBuffer = kKBytes + kVBytes + kScaleBytes;
+    static constexpr int kPieces = DP / 8;                                // of a row
+    static constexpr int kRowsAtOnce = 64 * kTileWaves / kPieces;
+    static constexpr int kPasses = kKeys / kRowsAtOnce;
+};
+
+template <class T, class F, int DP>
+__global__ __launch_bounds__(64 * kTileWaves, 2) void kvcache_attention_tile_kernel(const AttentionArgs a)
+{
+    typedef TileShape<DP> S;
+    typedef Held<T, F> H;
+    typedef typename H::V V;
+    typedef typename H::piece Piece;
+    __shared__ __align__(16) uint8_t lds[2 * S::kBuffer];
+
+    const uint32_t tid = threadIdx.x, lane = tid & 63u, half = lane >> 5, col = lane & 31u;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // key/value heads fastest: workgroups next to each other go to different
+    // XCDs, so the tiles of one head, which read the same keys, share an L2;
+    // the last tiles, with the most keys, come first
+    uint32_t x = blockIdx.x;
+    const uint32_t head = x % a.kv_heads;
+    x /= a.kv_heads;
+    const uint32_t split = x % a.splits;
+    const uint32_t tile = a.tiles - 1 - x / a.splits;
+    const Sequence seq = sequence_of(a, blockIdx.y);
+    const int32_t *table = a.table + blockIdx.y * a.table_stride;
+
+    const uint32_t rows = (uint32_t)seq.n * a.group.d;
+    const uint32_t row0 = tile * kTileRows;
+    if (row0 >= rows)
+        return;
+    const uint32_t row_last = (row0 + kTileRows < rows ? row0 + kTileRows : rows) - 1;
+    const int32_t shift = seq.ctx - seq.n;
+    const int32_t first = shift + (int32_t)a.group.div(row0), last = shift + (int32_t)a.group.div(row_last);
+    const KeyRange seen = key_range(first, last, a.window, seq.bound);
+    int32_t lo = seen.lo, hi = seen.hi;
+    if (a.splits > 1) {
+        const int32_t from = (int32_t)(split * a.split_keys), to = from + (int32_t)a.split_keys;
+        lo = lo > from ? lo : from;
+        hi = hi < to ? hi : to;
+    }
+
+    // this lane's row
+    const uint32_t row = row0 + wave * 32 + col;
+    const bool held = row < rows;
+    const uint32_t token = a.group.div(held ? row : 0), member = a.group.mod(held ? row : 0, token);
+    const int32_t pos = shift + (int32_t)token;
+    const int32_t see_hi = held ? (pos < hi - 1 ? pos : hi - 1) : -1;                 // last key seen
+    const int32_t see_lo = a.window > 0 ? pos - a.window + 1 : 0;
+
+    typename T::eight q[DP / 16];
+    {
+        const typename T::elem *at = (const typename T::elem *)a.q + (int64_t)(seq.q0 + token) * a.q_st +
+                                     (int64_t)(head * a.group.d + member) * a.q_sh;
+#pragma unroll
+        for (int s = 0; s < DP / 16; ++s) {
+            const uint32_t d = s * 16 + half * 8;
+            u32x4 p = {};
+            if (held && d < a.head_dim)
+                p = (*(const u32x4 *)(at + d) & a.q_keep) ^ a.q_flip;
+            q[s] = __builtin_bit_cast(typename T::eight, p);
+        }
+    }
+
+    f32x16 o[DP / 32] = {};
+    float m = -__builtin_inff(), l = 0.0f;
+
+    // rows of the next tile on their way: thread tid takes piece tid % kPieces
+    // of key tid / kPieces + i * kRowsAtOnce
+    const uint32_t piece = tid % S::kPieces, key0 = tid / S::kPieces;
+    const bool in = piece * 8 < a.head_dim;
+    const uint32_t esize = H::coded ? 1 : 2;
+    const uint8_t *kbase = (const uint8_t *)a.k + ((int64_t)head * a.k_head + piece * 8) * esize;
+    const uint8_t *vbase = (const uint8_t *)a.v + ((int64_t)head * a.v_head + piece * 8) * esize;
+    Place at[S::kPasses], scale_at;
+    Piece kp[S::kPasses], vp[S::kPasses];
+    float ks = 0.0f, vs = 0.0f;
+
+    auto look_up = [&](int32_t t0) {
+#pragma unroll
+        for (int i = 0; i < S::kPasses; ++i)
+            at[i] = place_of(a, table, t0 + (int32_t)key0 + i * S::kRowsAtOnce, hi);
+        if (H::coded && tid < S::kKeys)
+            scale_at = place_of(a, table, t0 + (int32_t)tid, hi);
+    };
+    auto load = [&]() {
+#pragma unroll
+        for (int i = 0; i < S::kPasses; ++i) {
+            kp[i] = Piece{};
+            vp[i] = Piece{};
+            if (in && at[i].page != ~0u) {
+                kp[i] = *(const Piece *)(kbase + page_offset(at[i].page, at[i].place, a.k_page, a.k_place) * esize);
+                vp[i] = *(const Piece *)(vbase + page_offset(at[i].page, at[i].place, a.v_page, a.v_place) * esize);
+            }
+        }
+        if (H::coded && tid < S::kKeys) {
+            ks = vs = 0.0f;
+            if (scale_at.page != ~0u) {
+                ks = a.k_scale[page_offset(scale_at.page, scale_at.place, a.ks_page, a.ks_place) + head * a.ks_head];
+                vs = a.v_scale[page_offset(scale_at.page, scale_at.place, a.vs_page, a.vs_place) + head * a.vs_head];
+            }
+        }
+    };
+    auto put = [&](uint8_t *buf) {
+#pragma unroll
+        for (int i = 0; i < S::kPasses; ++i) {
+            const uint32_t key = key0 + i * S::kRowsAtOnce;
+            *(u32x4 *)(buf + key * S::kKStride + piece * 16) = H::key(kp[i]);
+            *(u32x4 *)(buf + S::kKBytes + key * S::kVStride + piece * 16) = H::value(vp[i]);
+        }
+        if (H::coded && tid < S::kKeys) {
+            ((float *)(buf + S::kKBytes + S::kVBytes))[tid] = ks;
+            ((float *)(buf + S::kKBytes + S::kVBytes))[S::kKeys + tid] = vs;
+        }
+    };
+
+    if (lo < hi) {
+        look_up(lo);
+        load();
+        look_up(lo + S::kKeys);
+        put(lds);
+    }
+    __syncthreads();
+
+    uint32_t turn = 0;
+    for (int32_t t0 = lo; t0 < hi; t0 += S::kKeys, turn ^= 1) {
+        const uint8_t *buf = lds + turn * S::kBuffer;
+        const bool more = t0 + S::kKeys < hi;
+        if (more) {
+            load();
+            look_up(t0 + 2 * S::kKeys);
+        }
+        const float *kscale = (const float *)(buf + S::kKBytes + S::kVBytes);
+        const float *vscale = kscale + S::kKeys;
+
+        // scores
+        f32x16 s[S::kKeys / 32];
+#pragma unroll
+        for (int b = 0; b < S::kKeys / 32; ++b) {
+            s[b] = f32x16{};
+            const uint8_t *kat = buf + (b * 32 + col) * S::kKStride + half * 16;
+#pragma unroll
+            for (int i = 0; i < DP / 16; ++i)
+                s[b] = T::mfma32(*(const typename T::eight *)(kat + i * 32), q[i], s[b]);
+        }
+        // register 4 i + j of block b is key t0 + 32 b + 8 i + 4 half + j
+        if (H::coded) {
+#pragma unroll
+            for (int b = 0; b < S::kKeys / 32; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const f32x4 c = *(const f32x4 *)(kscale + b * 32 + i * 8 + half * 4);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        s[b][4 * i + j] *= c[j];
+                }
+        }
+        // not every row sees every key
+        const bool edge = t0 + S::kKeys - 1 > first || t0 + S::kKeys > hi ||
+                          (a.window > 0 && t0 <= last - a.window);
+        if (edge) {
+#pragma unroll
+            for (int b = 0; b < S::kKeys / 32; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int32_t t = t0 + b * 32 + (i / 4) * 8 + (int32_t)half * 4 + i % 4;
+                    s[b][i] = t <= see_hi && t >= see_lo ? s[b][i] : -__builtin_inff();
+                }
+        }
+
+        // the running maximum, in units of log2
+        float top = s[0][0];
+#pragma unroll
+        for (int b = 0; b < S::kKeys / 32; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                top = __builtin_fmaxf(top, s[b][i]);
+        top = __builtin_fmaxf(top, other_half(top)) * a.scale_log2;
+        if (__builtin_amdgcn_ballot_w64(top > m + kSlack)) {
+            const float grown = __builtin_fmaxf(m, top);
+            const float shrink = m == grown ? 1.0f : __builtin_amdgcn_exp2f(m - grown);
+            m = grown;
+            l *= shrink;
+#pragma unroll
+            for (int d = 0; d < DP / 32; ++d)
+                o[d] *= shrink;
+        }
+        const float base = m == -__builtin_inff() ? 0.0f : m;
+
+        typename V::eight p[S::kKeys / 16];
+#pragma unroll
+        for (int b = 0; b < S::kKeys / 32; ++b) {
+            float w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][i], a.scale_log2, -base));
+                l += w[i];
+            }
+            if (H::coded) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const f32x4 c = *(const f32x4 *)(vscale + b * 32 + i * 8 + half * 4);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float y = w[4 * i + j] * c[j];
+                        // a hidden row's scale may be anything
+                        w[4 * i + j] = edge && s[b][4 * i + j] == -__builtin_inff() ? 0.0f : y;
+                    }
+                }
+            }
+            p[2 * b] = __builtin_bit_cast(typename V::eight, pack8<V>(w));
+            p[2 * b + 1] = __builtin_bit_cast(typename V::eight, pack8<V>(w + 8));
+        }
+
+        // values: of a block of 16 keys, p holds keys 4 half .. + 3 and 8 + 4 half .. + 3
+        const uint8_t *vat = buf + S::kKBytes + (half * 4 + (lane % 16) / 4) * S::kVStride +
+                             ((lane / 16) % 2) * 32 + (lane % 4) * 8;
+        bool special = false;
+        if (edge) {
+#pragma unroll 1
+            for (int i = 0; i < S::kKeys / 16; ++i)
+#pragma unroll
+                for (int d = 0; d < DP / 32; ++d)
+                    special |= any_special<V>(columns(vat + i * 16 * S::kVStride + d * 64, 8 * S::kVStride));
+            special = __builtin_amdgcn_ballot_w64(special) != 0;
+        }
+        if (!special) {
+#pragma unroll
+            for (int i = 0; i < S::kKeys / 16; ++i)
+#pragma unroll
+                for (int d = 0; d < DP / 32; ++d)
+                    o[d] = V::mfma32(__builtin_bit_cast(typename V::eight,
+                                                        columns(vat + i * 16 * S::kVStride + d * 64, 8 * S::kVStride)),
+                                     p[i], o[d]);
+        } else {
+            // infinities and NaN among the values: the finite ones as above,
+            // and for the others a count, with weight 1 for keys that are seen
+#pragma unroll
+            for (int d = 0; d < DP / 32; ++d) {
+                f32x16 marks = {};
+#pragma unroll
+                for (int i = 0; i < S::kKeys / 16; ++i) {
+                    u32x4 clean, mark;
+                    part_special<V>(columns(vat + i * 16 * S::kVStride + d * 64, 8 * S::kVStride), clean, mark);
+                    float one[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int32_t t = t0 + i * 16 + (j / 4) * 8 + (int32_t)half * 4 + j % 4;
+                        one[j] = t <= see_hi && t >= see_lo ? 1.0f : 0.0f;
+                    }
+                    o[d] = V::mfma32(__builtin_bit_cast(typename V::eight, clean), p[i], o[d]);
+                    marks = V::mfma32(__builtin_bit_cast(typename V::eight, mark),
+                                      __builtin_bit_cast(typename V::eight, pack8<V>(one)), marks);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    o[d][i] += special_of(marks[i]);
+            }
+        }
+
+        if (more)
+            put(lds + (turn ^ 1) * S::kBuffer);
+        __syncthreads();
+    }
+
+    l += other_half(l);
+    if (!held)
+        return;
+    const uint32_t qhead = head * a.group.d + member;
+    const int64_t qtoken = seq.q0 + token;
+    if (a.splits > 1) {
+        const int64_t part = ((int64_t)split * a.total_q + qtoken) * a.q_heads + qhead;
+        if (half == 0) {
+            a.part_ml[2 * part] = m;
+            a.part_ml[2 * part + 1] = l;
+        }
+        float *to = a.part_o + part * a.head_dim;
+#pragma unroll
+        for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t at_d = d * 32 + i * 8 + half * 4;
+                if (at_d < a.head_dim)
+                    *(f32x4 *)(to + at_d) = f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
+            }
+        return;
+    }
+    if (a.lse && half == 0)
+        a.lse[qtoken * a.l_st + qhead * a.l_sh] = l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l)) * kLn2;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    typename T::elem *to = (typename T::elem *)a.out + qtoken * a.o_st + qhead * a.o_sh;
+#pragma unroll
+    for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t at_d = d * 32 + i * 8 + half * 4;
+            float y[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                y[j] = o[d][4 * i + j] * inv;
+            if (at_d < a.head_dim)
+                store4<T>(to + at_d, y);
+        }
+}
+
+// ---- few rows ---------------------------------------------------------------
+//
+// At most 16 rows a (sequence, key/value head), as in a decode step: bound by
+// reading the cache, so everything serves to keep reads in flight.  The keys
+// of a split are dealt to the 4 wavefronts of a workgroup in steps of 32; each
+// keeps its own maximum, sum and output, joined at the end.  A wavefront takes
+// K straight from memory into the matrix instruction's registers, V through
+// registers into shared memory of its own (for the transposing read), and
+// issues the next step's reads as soon as a step's registers are free.
+
+template <int DP>
+struct SingleShape {
+    static constexpr int kVStride = DP * 2 + 32;   // 32 mod 256: see above, for blocks of 16 rows
+    static constexpr int kVBytes = kSingleKeys * kVStride;
+    static constexpr int kWaveBytes = kVBytes + kSingleKeys * 8;   // and the scales
+    static constexpr int kPieces = DP / 8;
+    static constexpr int kRowsAtOnce = 64 / kPieces;
+    static constexpr int kPasses = kSingleKeys / kRowsAtOnce;
+    static constexpr int kJoinBytes = kSingleWaves * kSingleRows * (DP + 4) * 4;
+    static constexpr int kBytes = kSingleWaves * kWaveBytes > kJoinBytes ? kSingleWaves * kWaveBytes : kJoinBytes;
+};
+
+template <class T, class F, int DP>
+__global__ __launch_bounds__(64 * kSingleWaves) void kvcache_attention_single_kernel(const AttentionArgs a)
+{
+    typedef SingleShape<DP> S;
+    typedef Held<T, F> H;
+    typedef typename H::V V;
+    typedef typename H::piece Piece;
+    __shared__ __align__(16) uint8_t lds[S::kBytes];
+    __shared__ float join_m[kSingleWaves][kSingleRows], join_l[kSingleWaves][kSingleRows];
+
+    const uint32_t tid = threadIdx.x, lane = tid & 63u, group = lane >> 4, col = lane & 15u;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t head = blockIdx.x % a.kv_heads, split = blockIdx.x / a.kv_heads;
+    const Sequence seq = sequence_of(a, blockIdx.y);
+    const int32_t *table = a.table + blockIdx.y * a.table_stride;
+    uint32_t rows = (uint32_t)seq.n * a.group.d;
+    rows = rows < kSingleRows ? rows : kSingleRows;   // more: flagged by sequence_of
+    if (rows == 0)
+        return;
+    const int32_t shift = seq.ctx - seq.n;
+    const int32_t first = shift, last = shift + (int32_t)a.group.div(rows - 1);
+    const KeyRange seen = key_range(first, last, a.window, seq.bound);
+    int32_t lo = seen.lo, hi = seen.hi;
+    {
+        const int32_t from = (int32_t)(split * a.split_keys), to = from + (int32_t)a.split_keys;
+        lo = lo > from ? lo : from;
+        hi = hi < to ? hi : to;
+    }
+
+    const bool held = col < rows;
+    const uint32_t token = a.group.div(held ? col : 0), member = a.group.mod(held ? col : 0, token);
+    const int32_t pos = shift + (int32_t)token;
+    const int32_t see_hi = held ? (pos < hi - 1 ? pos : hi - 1) : -1;
+    const int32_t see_lo = a.window > 0 ? pos - a.window + 1 : 0;
+
+    typename T::eight q[DP / 32];
+    {
+        const typename T::elem *at = (const typename T::elem *)a.q + (int64_t)(seq.q0 + token) * a.q_st +
+                                     (int64_t)(head * a.group.d + member) * a.q_sh;
+#pragma unroll
+        for (int s = 0; s < DP / 32; ++s) {
+            const uint32_t d = s * 32 + group * 8;
+            u32x4 p = {};
+            if (held && d < a.head_dim)
+                p = (*(const u32x4 *)(at + d) & a.q_keep) ^ a.q_flip;
+            q[s] = __builtin_bit_cast(typename T::eight, p);
+        }
+    }
+
+    uint8_t *vlds = lds + wave * S::kWaveBytes;
+    float *scales = (float *)(vlds + S::kVBytes);   // 32 of the keys, 32 of the values
+    f32x4 o[DP / 16] = {};
+    float m = -__builtin_inff(), l = 0.0f;
+
+    const uint32_t esize = H::coded ? 1 : 2;
+    const uint8_t *kbase = (const uint8_t *)a.k + ((int64_t)head * a.k_head + group * 8) * esize;
+    const uint32_t piece = lane % S::kPieces, vkey = lane / S::kPieces;
+    const uint8_t *vbase = (const uint8_t *)a.v + ((int64_t)head * a.v_head + piece * 8) * esize;
+    const bool vin = piece * 8 < a.head_dim;
+    Piece kp[2][DP / 32], vp[S::kPasses];
+    float ks = 0.0f, vs = 0.0f;
+    Place mine;   // lanes 0-31: of key `lane` of the next step
+
+    auto other = [&](uint32_t key) {
+        Place p;
+        p.page = __shfl(mine.page, key, 64);
+        p.place = __shfl(mine.place, key, 64);
+        return p;
+    };
+    auto load_keys = [&]() {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const Place p = other(b * 16 + col);
+            const uint8_t *at = kbase + page_offset(p.page, p.place, a.k_page, a.k_place) * esize;
+#pragma unroll
+            for (int s = 0; s < DP / 32; ++s) {
+                kp[b][s] = Piece{};
+                if (p.page != ~0u && s * 32 + group * 8 < a.head_dim)
+                    kp[b][s] = *(const Piece *)(at + s * 32 * esize);
+            }
+        }
+        if (H::coded) {
+            ks = vs = 0.0f;
+            if (lane < 32 && mine.page != ~0u) {
+                ks = a.k_scale[page_offset(mine.page, mine.place, a.ks_page, a.ks_place) + head * a.ks_head];
+                vs = a.v_scale[page_offset(mine.page, mine.place, a.vs_page, a.vs_place) + head * a.vs_head];
+            }
+        }
+    };
+    auto load_values = [&]() {
+#pragma unroll
+        for (int i = 0; i < S::kPasses; ++i) {
+            const Place p = other(i * S::kRowsAtOnce + vkey);
+            vp[i] = Piece{};
+            if (vin && p.page != ~0u)
+                vp[i] = *(const Piece *)(vbase + page_offset(p.page, p.place, a.v_page, a.v_place) * esize);
+        }
+    };
+
+    constexpr int kStep = kSingleKeys * kSingleWaves;
+    int32_t t0 = lo + (int32_t)wave * kSingleKeys;
+    mine = place_of(a, table, t0 + (int32_t)(lane & 31u), hi);
+    if (t0 < hi) {
+        load_keys();
+        load_values();
+    }
+    for (; t0 < hi; t0 += kStep) {
+        mine = place_of(a, table, t0 + kStep + (int32_t)(lane & 31u), hi);
+        f32x4 s[2] = {};
+#pragma unroll
+        for (int i = 0; i < DP / 32; ++i)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+                s[b] = T::mfma16(__builtin_bit_cast(typename T::eight, H::key(kp[b][i])), q[i], s[b]);
+        if (H::coded && lane < 32) {
+            scales[lane] = ks;
+            scales[32 + lane] = vs;
+        }
+#pragma unroll
+        for (int i = 0; i < S::kPasses; ++i)
+            *(u32x4 *)(vlds + (i * S::kRowsAtOnce + vkey) * S::kVStride + piece * 16) = H::value(vp[i]);
+        // the wavefront's own writes, read back by other lanes of it: in order
+        // in the LDS queue, and kept in order by the compiler
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (t0 + kStep < hi) {
+            load_keys();
+            load_values();
+        }
+
+        // register j of block b is key t0 + 16 b + 4 group + j
+        f32x4 vscale[2];
+        if (H::coded) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                s[b] *= *(const f32x4 *)(scales + b * 16 + group * 4);
+                vscale[b] = *(const f32x4 *)(scales + 32 + b * 16 + group * 4);
+            }
+        }
+        const bool edge = t0 + kSingleKeys - 1 > first || t0 + kSingleKeys > hi ||
+                          (a.window > 0 && t0 <= last - a.window);
+        if (edge) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int32_t t = t0 + b * 16 + (int32_t)group * 4 + j;
+                    s[b][j] = t <= see_hi && t >= see_lo ? s[b][j] : -__builtin_inff();
+                }
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                top = __builtin_fmaxf(top, s[b][j]);
+        top = __builtin_fmaxf(top, other_half(top));
+        top = __builtin_fmaxf(top, __shfl_xor(top, 16, 64)) * a.scale_log2;
+        if (__builtin_amdgcn_ballot_w64(top > m + kSlack)) {
+            const float grown = __builtin_fmaxf(m, top);
+            const float shrink = m == grown ? 1.0f : __builtin_amdgcn_exp2f(m - grown);
+            m = grown;
+            l *= shrink;
+#pragma unroll
+            for (int d = 0; d < DP / 16; ++d)
+                o[d] *= shrink;
+        }
+        const float base = m == -__builtin_inff() ? 0.0f : m;
+        float w[8];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                w[4 * b + j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][j], a.scale_log2, -base));
+                l += w[4 * b + j];
+                if (H::coded) {
+                    const float y = w[4 * b + j] * vscale[b][j];
+                    w[4 * b + j] = edge && s[b][j] == -__builtin_inff() ? 0.0f : y;
+                }
+            }
+        const typename V::eight p = __builtin_bit_cast(typename V::eight, pack8<V>(w));
+
+        // keys 4 group .. + 3 and 16 + 4 group .. + 3, columns 16 d + lane % 16
+        const uint8_t *vat = vlds + (group * 4 + col / 4) * S::kVStride + (col % 4) * 8;
+        bool special = false;
+        if (edge) {
+#pragma unroll
+            for (int d = 0; d < DP / 16; ++d)
+                special |= any_special<V>(columns(vat + d * 32, 16 * S::kVStride));
+            special = __builtin_amdgcn_ballot_w64(special) != 0;
+        }
+        if (!special) {
+#pragma unroll
+            for (int d = 0; d < DP / 16; ++d)
+                o[d] = V::mfma16(__builtin_bit_cast(typename V::eight, columns(vat + d * 32, 16 * S::kVStride)), p, o[d]);
+        } else {
+            float one[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int32_t t = t0 + (j / 4) * 16 + (int32_t)group * 4 + j % 4;
+                one[j] = t <= see_hi && t >= see_lo ? 1.0f : 0.0f;
+            }
+            const typename V::eight ones = __builtin_bit_cast(typename V::eight, pack8<V>(one));
+#pragma unroll
+            for (int d = 0; d < DP / 16; ++d) {
+                u32x4 clean, mark;
+                part_special<V>(columns(vat + d * 32, 16 * S::kVStride), clean, mark);
+                o[d] = V::mfma16(__builtin_bit_cast(typename V::eight, clean), p, o[d]);
+                const f32x4 marks = V::mfma16(__builtin_bit_cast(typename V::eight, mark), ones, f32x4{});
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    o[d][j] += special_of(marks[j]);
+            }
+        }
+        // the next step's writes stay behind these reads
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+
+    // join the four wavefronts
+    l += other_half(l);
+    l += __shfl_xor(l, 16, 64);
+    if (lane < 16) {
+        join_m[wave][col] = m;
+        join_l[wave][col] = l;
+    }
+    __syncthreads();   // also: every wavefront is done with its V
+    float top = -__builtin_inff(), sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kSingleWaves; ++w)
+        top = __builtin_fmaxf(top, join_m[w][col]);
+    const float base = top == -__builtin_inff() ? 0.0f : top;
+    float *joined = (float *)lds;   // [wave][row][DP + 4]
+    {
+        const float f = m == top ? 1.0f : __builtin_amdgcn_exp2f(m - base);
+        float *to = joined + (wave * kSingleRows + col) * (DP + 4);
+#pragma unroll
+        for (int d = 0; d < DP / 16; ++d)
+            *(f32x4 *)(to + d * 16 + group * 4) = o[d] * f;
+    }
+    __syncthreads();
+    // a thread takes 4 columns of a row
+    for (uint32_t i = tid; i < rows * (DP / 4); i += 64 * kSingleWaves) {
+        const uint32_t r = i / (DP / 4), d = i % (DP / 4) * 4;
+        if (d >= a.head_dim)
+            continue;
+        f32x4 y = {};
+#pragma unroll
+        for (int w = 0; w < kSingleWaves; ++w)
+            y += *(const f32x4 *)(joined + (w * kSingleRows + r) * (DP + 4) + d);
+        float rtop = -__builtin_inff();
+#pragma unroll
+        for (int w = 0; w < kSingleWaves; ++w)
+            rtop = __builtin_fmaxf(rtop, join_m[w][r]);
+        sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kSingleWaves; ++w)
+            sum += join_m[w][r] == rtop ? join_l[w][r]
+                                        : join_l[w][r] * __builtin_amdgcn_exp2f(join_m[w][r] - rtop);
+        const uint32_t tok = a.group.div(r), qhead = head * a.group.d + a.group.mod(r, tok);
+        const int64_t qtoken = seq.q0 + tok;
+        if (a.splits > 1) {
+            const int64_t part = ((int64_t)split * a.total_q + qtoken) * a.q_heads + qhead;
+            if (d == 0) {
+                a.part_ml[2 * part] = rtop;
+                a.part_ml[2 * part + 1] = sum;
+            }
+            *(f32x4 *)(a.part_o + part * a.head_dim + d) = y;
+        } else {
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const float z[4] = {y.x * inv, y.y * inv, y.z * inv, y.w * inv};
+            store4<T>((typename T::elem *)a.out + qtoken * a.o_st + qhead * a.o_sh + d, z);
+            if (a.lse && d == 0)
+                a.lse[qtoken * a.l_st + qhead * a.l_sh] =
+                    sum == 0.0f ? -__builtin_inff() : (rtop + __builtin_log2f(sum)) * kLn2;
+        }
+    }
+}
+
+// ---- joining splits ---------------------------------------------------------
+//
+// A wavefront to a row: out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s,
+// in the order of the splits.  A split without keys has l = 0 and is not read.
+
+template <class T>
+__global__ __launch_bounds__(256) void kvcache_attention_join_kernel(const AttentionArgs a)
+{
+    const uint32_t lane = threadIdx.x & 63u;
+    const int64_t rows = (int64_t)a.total_q * a.q_heads;
+    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (row >= rows)
+        return;
+    float m = -__builtin_inff();
+    for (uint32_t s = 0; s < a.splits; ++s) {
+        if (a.part_ml[2 * (s * rows + row) + 1] != 0.0f)
+            m = __builtin_fmaxf(m, a.part_ml[2 * (s * rows + row)]);
+    }
+    float l = 0.0f;
+    f32x4 y = {};
+    const uint32_t d = lane * 4;
+    for (uint32_t s = 0; s < a.splits; ++s) {
+        const float ms = a.part_ml[2 * (s * rows + row)], ls = a.part_ml[2 * (s * rows + row) + 1];
+        if (ls == 0.0f)
+            continue;
+        const float f = ms == m ? 1.0f : __builtin_amdgcn_exp2f(ms - m);
+        l += ls * f;
+        if (d < a.head_dim)
+            y += *(const f32x4 *)(a.part_o + (s * rows + row) * a.head_dim + d) * f;
+    }
+    const int64_t token = row / a.q_heads, head = row % a.q_heads;
+    if (a.lse && lane == 0)
+        a.lse[token * a.l_st + head * a.l_sh] = l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l)) * kLn2;
+    if (d < a.head_dim) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const float z[4] = {y.x * inv, y.y * inv, y.z * inv, y.w * inv};
+        store4<T>((typename T::elem *)a.out + token * a.o_st + head * a.o_sh + d, z);
+    }
+}
+
+template <class T, class F, int DP>
+void attention_pick(const AttentionArgs &a, const AttentionShape &shape, uint32_t num_seqs, hipStream_t s)
+{
+    if (shape.single)
+        hipLaunchKernelGGL((kvcache_attention_single_kernel<T, F, DP>), dim3(a.kv_heads * a.splits, num_seqs),
+                           dim3(64 * kSingleWaves), 0, s, a);
+    else
+        hipLaunchKernelGGL((kvcache_attention_tile_kernel<T, F, DP>),
+                           dim3(a.kv_heads * a.splits * a.tiles, num_seqs), dim3(64 * kTileWaves), 0, s, a);
+}
+
+template <class T, class F>
+void attention_dim(const AttentionArgs &a, const AttentionShape &shape, uint32_t num_seqs, hipStream_t s)
+{
+    if (a.head_dim <= 64)
+        attention_pick<T, F, 64>(a, shape, num_seqs, s);
+    else if (a.head_dim <= 128)
+        attention_pick<T, F, 128>(a, shape, num_seqs, s);
+    else
+        attention_pick<T, F, 256>(a, shape, num_seqs, s);
+}
+
+template <class T>
+hipError_t attention_type(const AttentionArgs &a, const AttentionShape &shape, uint32_t num_seqs,
+                          uint32_t format, hipStream_t s)
+{
+    if (format == KVCACHE_FP8)
+        attention_dim<T, Fp8>(a, shape, num_seqs, s);
+    else if (format == KVCACHE_INT8)
+        attention_dim<T, Int8>(a, shape, num_seqs, s);
+    else
+        attention_dim<T, void>(a, shape, num_seqs, s);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.splits == 1)
+        return e;
+    const uint64_t rows = (uint64_t)a.total_q * a.q_heads;
+    hipLaunchKernelGGL((kvcache_attention_join_kernel<T>), dim3((uint32_t)((rows + 3) / 4)), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+// The layout of a call.  Workgroups wanted: `kFill`, about three to each of
+// 256 CUs (two of the tile kernel); where the rows give fewer, the keys are
+// split, into no fewer than kSplitKeys each.
+AttentionShape attention_shape(uint32_t num_seqs, uint32_t total_q, uint32_t q_heads, uint32_t kv_heads,
+                               uint32_t head_dim, uint32_t max_q_len, uint32_t max_context,
+                               uint32_t window)
+{
+    AttentionShape r = {};
+    const uint64_t rows = (uint64_t)max_q_len * (q_heads / kv_heads);
+    r.single = rows <= (uint64_t)kSingleRows;
+    r.tiles = r.single ? 1 : (uint32_t)((rows + kTileRows - 1) / kTileRows);
+    const uint64_t fill = r.single ? 768 : 512;
+    const uint64_t blocks = (uint64_t)num_seqs * kv_heads * r.tiles;
+    const uint32_t least = r.single ? 256 : 512;
+    (void)window;
+    uint64_t splits = blocks ? fill / blocks : 1;
+    const uint64_t most = (max_context + least - 1) / least;
+    splits = splits < most ? splits : most;
+    splits = splits ? splits : 1;
+    const uint32_t unit = 128;
+    uint64_t keys = ((uint64_t)max_context + splits - 1) / splits;
+    keys = (keys + unit - 1) / unit * unit;
+    keys = keys ? keys : unit;
+    r.split_keys = (uint32_t)keys;
+    r.splits = (uint32_t)((max_context + keys - 1) / keys);
+    r.splits = r.splits ? r.splits : 1;
+    if (r.splits > 1)
+        r.workspace_bytes = (uint64_t)r.splits * total_q * q_heads * (head_dim + 2) * 4;
+    return r;
+}
+
+hipError_t launch_attention(const AttentionArgs &a, const AttentionShape &shape, uint32_t num_seqs,
+                            uint32_t dtype, uint32_t format, hipStream_t stream)
+{
+    if (dtype == KVCACHE_BF16)
+        return attention_type<Bf16>(a, shape, num_seqs, format, stream);
+    return attention_type<Fp16>(a, shape, num_seqs, format, stream);
+}
+
+}  // namespace kvc

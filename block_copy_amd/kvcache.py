@@ -1,0 +1,304 @@
+"""ctypes binding of the cache operators of libkvcopy.so (include/kvcache.h)
+for torch tensors: rotary positions, writes into and reads from paged key/value
+caches, and attention of new tokens over them.
+
+Every step runs inside the library; this module checks shapes, types and
+devices and passes addresses.  Work is enqueued on `stream` (a
+torch.cuda.Stream or a raw handle), by default torch's current stream of the
+tensors' device.  As with any call on another stream, a tensor used on a stream
+other than the one it was made on has to be kept until that work is done
+(Tensor.record_stream, or an event).
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from .kvcopy import EALIGN, EHIP, EINVAL, KvcopyError, OK, lib  # noqa: F401
+
+BF16, FP16, FP32, FP8, INT8 = 0, 1, 2, 3, 4
+BAD_PAGE, BAD_SLOT, BAD_LENGTH = 1, 2, 4
+ROPE_INTERLEAVED, ROPE_INVERSE = 1, 2
+MAX_HEAD_DIM, MAX_ATTENTION_HEAD_DIM = 512, 256
+SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
+
+EXPORTS = ("kvcache_rope_frequencies", "kvcache_rope", "kvcache_write", "kvcache_read",
+           "kvcache_attention_workspace_bytes", "kvcache_attention")
+
+_TYPES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32,
+          torch.float8_e4m3fn: FP8, torch.int8: INT8}
+
+
+class Rows(ctypes.Structure):
+    """kvcache_rows_t."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+_S3 = ctypes.c_int64 * 3
+
+
+class Pages(ctypes.Structure):
+    """kvcache_pages_t."""
+    _fields_ = [("struct_size", ctypes.c_uint32), ("format", ctypes.c_uint32),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("k_stride", _S3), ("v_stride", _S3), ("ks_stride", _S3), ("vs_stride", _S3),
+                ("num_pages", ctypes.c_uint64), ("kv_heads", ctypes.c_uint32),
+                ("page_size", ctypes.c_uint32), ("head_dim", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32)]
+
+
+class Rope(ctypes.Structure):
+    """kvcache_rope_t."""
+    _fields_ = [("struct_size", ctypes.c_uint32), ("dtype", ctypes.c_uint32),
+                ("flags", ctypes.c_uint32), ("factor", ctypes.c_float),
+                ("positions", ctypes.c_void_p), ("freq", ctypes.c_void_p),
+                ("tokens", ctypes.c_uint64), ("head_dim", ctypes.c_uint32),
+                ("rot_dim", ctypes.c_uint32), ("q_heads", ctypes.c_uint32),
+                ("k_heads", ctypes.c_uint32), ("q", Rows), ("k", Rows), ("q_out", Rows),
+                ("k_out", Rows)]
+
+
+class AttentionArgs(ctypes.Structure):
+    """kvcache_attention_t."""
+    _fields_ = [("struct_size", ctypes.c_uint32), ("dtype", ctypes.c_uint32), ("q", Rows),
+                ("out", Rows), ("lse", ctypes.c_void_p), ("lse_token_stride", ctypes.c_int64),
+                ("lse_head_stride", ctypes.c_int64), ("page_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("q_starts", ctypes.c_void_p),
+                ("context_lens", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_uint64), ("status", ctypes.c_void_p),
+                ("num_seqs", ctypes.c_uint32), ("q_heads", ctypes.c_uint32),
+                ("table_columns", ctypes.c_uint32), ("total_q", ctypes.c_uint32),
+                ("max_q_len", ctypes.c_uint32), ("max_context", ctypes.c_uint32),
+                ("window", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+def _declare():
+    p, u32, u64 = ctypes.c_void_p, ctypes.c_uint32, ctypes.c_uint64
+    pages, rows = ctypes.POINTER(Pages), ctypes.POINTER(Rows)
+    lib.kvcache_rope_frequencies.restype = ctypes.c_int
+    lib.kvcache_rope_frequencies.argtypes = [p, u32, ctypes.c_double, ctypes.c_int, ctypes.c_double,
+                                             u32, ctypes.c_double, ctypes.c_double]
+    lib.kvcache_rope.restype = ctypes.c_int
+    lib.kvcache_rope.argtypes = [ctypes.POINTER(Rope), p]
+    for f in (lib.kvcache_write, lib.kvcache_read):
+        f.restype = ctypes.c_int
+        f.argtypes = [pages, u32, rows, rows, p, u64, p, p]
+    lib.kvcache_attention_workspace_bytes.restype = u64
+    lib.kvcache_attention_workspace_bytes.argtypes = [pages, ctypes.POINTER(AttentionArgs)]
+    lib.kvcache_attention.restype = ctypes.c_int
+    lib.kvcache_attention.argtypes = [pages, ctypes.POINTER(AttentionArgs), p]
+
+
+_declare()
+
+
+def _check(rc: int, where: str) -> None:
+    if rc != OK:
+        raise KvcopyError(rc, where)
+
+
+def _require(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _call(fn, where: str, device, stream, *args) -> None:
+    """fn(*args, stream) with `device` current."""
+    index = device.index
+    if stream is None:
+        handle = torch.cuda.current_stream(device).cuda_stream
+    else:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch.cuda.current_device() == index:
+        _check(fn(*args, handle), where)
+    else:
+        with torch.cuda.device(index):
+            _check(fn(*args, handle), where)
+
+
+def _status(status, device):
+    if status is None:
+        return None
+    _require(status.device == device and status.dtype in (torch.int32, torch.uint32)
+             and status.numel() >= 1, "status must be an int32 tensor on the same device")
+    return status.data_ptr()
+
+
+def _vector(t, dtype, n, device, what):
+    _require(t.dtype == dtype and t.device == device and t.dim() == 1 and t.shape[0] == n
+             and (n <= 1 or t.stride(0) == 1),
+             f"{what} must be a contiguous {dtype} vector of {n} on {device}")
+    return t.data_ptr()
+
+
+def _rows(t, shape, dtype, device, what):
+    _require(t.dtype == dtype and t.device == device and tuple(t.shape) == shape,
+             f"{what} must be {dtype} of shape {shape} on {device}")
+    st = t.stride()
+    _require(st[2] == 1 or shape[2] == 1, f"{what}: the last dimension must be contiguous")
+    return Rows(t.data_ptr(), st[0], st[1])
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none",
+                     factor: float = 1.0, original: int = 0, low: float = 1.0,
+                     high: float = 4.0, device=None) -> torch.Tensor:
+    """Radians per position of each pair, float64 (kvcache_rope_frequencies);
+    scaling: "none", "linear", "base" or "parts"."""
+    _require(scaling in SCALINGS, f"scaling must be one of {sorted(SCALINGS)}")
+    out = torch.empty(max(1, int(rot_dim) // 2), dtype=torch.float64)
+    _check(lib.kvcache_rope_frequencies(out.data_ptr(), int(rot_dim), float(base),
+                                        SCALINGS[scaling], float(factor), int(original),
+                                        float(low), float(high)), "kvcache_rope_frequencies")
+    return out if device is None else out.to(device)
+
+
+def rope(positions, freqs, q, k=None, *, q_out=None, k_out=None, interleaved: bool = False,
+         factor: float = 1.0, inverse: bool = False, stream=None):
+    """Turns q (and k), [tokens, heads, head_dim], by rotary positions (see
+    kvcache_rope): positions int32 [tokens], freqs float64 [rot_dim / 2].
+    q_out and k_out default to new tensors and may be q and k themselves.
+    Returns (q_out, k_out)."""
+    _require(q.dim() == 3 and q.is_cuda and q.dtype in (torch.bfloat16, torch.float16, torch.float32),
+             "q must be a [tokens, heads, head_dim] bfloat16, float16 or float32 GPU tensor")
+    dev, dt = q.device, q.dtype
+    tokens, heads, dim = q.shape
+    a = Rope(ctypes.sizeof(Rope), _TYPES[dt],
+             (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0), factor)
+    a.positions = _vector(positions, torch.int32, tokens, dev, "positions")
+    a.freq = _vector(freqs, torch.float64, freqs.shape[0], dev, "freqs")
+    a.tokens, a.head_dim, a.rot_dim, a.q_heads = tokens, dim, 2 * freqs.shape[0], heads
+    if q_out is None:
+        q_out = torch.empty((tokens, heads, dim), dtype=dt, device=dev)
+    a.q, a.q_out = _rows(q, (tokens, heads, dim), dt, dev, "q"), _rows(q_out, (tokens, heads, dim), dt, dev, "q_out")
+    if k is not None:
+        _require(k.dim() == 3, "k must be [tokens, heads, head_dim]")
+        shape = (tokens, k.shape[1], dim)
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=dt, device=dev)
+        a.k_heads = k.shape[1]
+        a.k, a.k_out = _rows(k, shape, dt, dev, "k"), _rows(k_out, shape, dt, dev, "k_out")
+    else:
+        _require(k_out is None, "k_out without k")
+    _call(lib.kvcache_rope, "kvcache_rope", dev, stream, ctypes.byref(a))
+    return q_out, k_out
+
+
+class PagedCache:
+    """Keys and values in pages [num_pages, kv_heads, page_size, head_dim]
+    (views in any memory order with the last dimension contiguous):
+    bfloat16 or float16, or float8_e4m3fn or int8 codes with float32 scales
+    [num_pages, kv_heads, page_size].  Holds the tensors; the memory stays the
+    caller's."""
+
+    def __init__(self, k, v, k_scales=None, v_scales=None):
+        _require(k.dim() == 4 and k.is_cuda and k.dtype in _TYPES and k.dtype != torch.float32,
+                 "pages must be 4-dimensional bfloat16, float16, float8_e4m3fn or int8 GPU tensors")
+        _require(v.shape == k.shape and v.dtype == k.dtype and v.device == k.device,
+                 "k and v must have the same shape, type and device")
+        coded = k.dtype in (torch.float8_e4m3fn, torch.int8)
+        _require(coded == (k_scales is not None) and coded == (v_scales is not None),
+                 "8-bit pages need k_scales and v_scales, others take none")
+        p = Pages(ctypes.sizeof(Pages), _TYPES[k.dtype], k.data_ptr(), v.data_ptr())
+        for x, name in ((k, "k_stride"), (v, "v_stride")):
+            _require(x.stride(3) == 1 or x.shape[3] == 1, "head_dim must be contiguous")
+            setattr(p, name, _S3(*x.stride()[:3]))
+        if coded:
+            for x, name in ((k_scales, "ks_stride"), (v_scales, "vs_stride")):
+                _require(x.shape == k.shape[:3] and x.dtype == torch.float32 and x.device == k.device,
+                         "scales must be float32 of shape [num_pages, kv_heads, page_size]")
+                setattr(p, name, _S3(*x.stride()))
+            p.k_scale, p.v_scale = k_scales.data_ptr(), v_scales.data_ptr()
+        p.num_pages, p.kv_heads, p.page_size, p.head_dim = k.shape
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self.dtype, self.device, self.coded = k.dtype, k.device, coded
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        self.pages, self._ref = p, ctypes.byref(p)
+
+
+def write(cache: PagedCache, k, v, slots, *, status=None, stream=None) -> None:
+    """Writes k and v, [tokens, kv_heads, head_dim], to slots (int64 [tokens];
+    negative: left out) of the cache (see kvcache_write)."""
+    _require(k.dim() == 3 and k.dtype in (torch.bfloat16, torch.float16), "k must be a 3-dimensional 16-bit tensor")
+    dev, shape = cache.device, (k.shape[0], cache.kv_heads, cache.head_dim)
+    r, w = _rows(k, shape, k.dtype, dev, "k"), _rows(v, shape, k.dtype, dev, "v")
+    _call(lib.kvcache_write, "kvcache_write", dev, stream, cache._ref, _TYPES[k.dtype], ctypes.byref(r),
+          ctypes.byref(w), _vector(slots, torch.int64, shape[0], dev, "slots"), shape[0], _status(status, dev))
+
+
+def read(cache: PagedCache, slots, k_out=None, v_out=None, *, dtype=None, status=None, stream=None):
+    """The values at slots (int64 [tokens]; negative: zeros) of the cache, in
+    k_out and v_out, [tokens, kv_heads, head_dim] (see kvcache_read); new
+    tensors of `dtype` (bfloat16, or the pages' own) where not given.
+    Returns (k_out, v_out)."""
+    dev, shape = cache.device, (slots.shape[0], cache.kv_heads, cache.head_dim)
+    if dtype is None:
+        given = k_out if k_out is not None else v_out
+        dtype = given.dtype if given is not None else torch.bfloat16 if cache.coded else cache.dtype
+    _require(dtype in (torch.bfloat16, torch.float16, torch.float32), "rows are bfloat16, float16 or float32")
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=dev)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=dev)
+    r, w = _rows(k_out, shape, dtype, dev, "k_out"), _rows(v_out, shape, dtype, dev, "v_out")
+    _call(lib.kvcache_read, "kvcache_read", dev, stream, cache._ref, _TYPES[dtype], ctypes.byref(r),
+          ctypes.byref(w), _vector(slots, torch.int64, shape[0], dev, "slots"), shape[0], _status(status, dev))
+    return k_out, v_out
+
+
+class AttentionPlan:
+    """Attention of new tokens over a cache (see kvcache_attention), for up to
+    num_seqs sequences and total_q new tokens: the sizes and the workspace that
+    calls of one shape share.  A plan serves one call at a time; calls on
+    different streams need plans of their own.
+
+    scale defaults to 1 / sqrt(head_dim); window 0 means none.  num_seqs and
+    total_q are exact; max_q_len and max_context are bounds."""
+
+    def __init__(self, cache: PagedCache, *, q_heads: int, num_seqs: int, total_q: int, max_q_len: int,
+                 max_context: int, window: int = 0, scale=None, dtype=None):
+        self.cache = cache
+        self.dtype = dtype if dtype is not None else torch.bfloat16 if cache.coded else cache.dtype
+        _require(self.dtype in (torch.bfloat16, torch.float16), "rows are bfloat16 or float16")
+        a = AttentionArgs(ctypes.sizeof(AttentionArgs), _TYPES[self.dtype])
+        a.num_seqs, a.q_heads, a.total_q = num_seqs, q_heads, total_q
+        a.max_q_len, a.max_context, a.window = max_q_len, max_context, window
+        a.scale = 1.0 / math.sqrt(cache.head_dim) if scale is None else scale
+        # columns are checked against the table of each call
+        a.table_columns = -(-max_context // cache.page_size)
+        self.columns = a.table_columns
+        probe = lib.kvcache_attention_workspace_bytes(cache._ref, ctypes.byref(a))
+        self.workspace = torch.empty(probe, dtype=torch.uint8, device=cache.device) if probe else None
+        if probe:
+            a.workspace, a.workspace_bytes = self.workspace.data_ptr(), probe
+        self.args, self._ref = a, ctypes.byref(a)
+        self.shape, self.num_seqs = (total_q, q_heads, cache.head_dim), num_seqs
+
+    def __call__(self, q, page_table, q_starts, context_lens, *, out=None, lse=None, status=None, stream=None):
+        """q [total_q, q_heads, head_dim]; page_table int32 [num_seqs, columns];
+        q_starts int32 [num_seqs + 1]; context_lens int32 [num_seqs].  lse, if
+        given, float32 [total_q, q_heads], receives the log-sums.  Returns out."""
+        a, dev = self.args, self.cache.device
+        if out is None:
+            out = torch.empty(self.shape, dtype=self.dtype, device=dev)
+        a.q = _rows(q, self.shape, self.dtype, dev, "q")
+        a.out = _rows(out, self.shape, self.dtype, dev, "out")
+        _require(page_table.dtype == torch.int32 and page_table.device == dev and page_table.dim() == 2
+                 and page_table.shape[0] == self.num_seqs and page_table.shape[1] >= self.columns
+                 and (page_table.shape[1] <= 1 or page_table.stride(1) == 1),
+                 f"page_table must be int32 [{self.num_seqs}, >= {self.columns}] with contiguous rows on {dev}")
+        a.page_table, a.table_stride = page_table.data_ptr(), page_table.stride(0)
+        a.q_starts = _vector(q_starts, torch.int32, self.num_seqs + 1, dev, "q_starts")
+        a.context_lens = _vector(context_lens, torch.int32, self.num_seqs, dev, "context_lens")
+        if lse is not None:
+            _require(lse.dtype == torch.float32 and lse.device == dev and tuple(lse.shape) == self.shape[:2],
+                     f"lse must be float32 {self.shape[:2]} on {dev}")
+            a.lse, a.lse_token_stride, a.lse_head_stride = lse.data_ptr(), lse.stride(0), lse.stride(1)
+        else:
+            a.lse = None
+        a.status = _status(status, dev)
+        _call(lib.kvcache_attention, "kvcache_attention", dev, stream, self.cache._ref, self._ref)
+        return out
