@@ -22,8 +22,9 @@
 //
 // What a row does not see is not read, or its score is set to -infinity; a
 // value row that some rows of a tile see and others do not is multiplied by an
-// exact 0 for the latter, except that 0 * infinity is NaN: tiles at the mask's
-// edge look for such values and take the long way (`hidden_product`).
+// exact 0 for the latter, except that 0 * infinity is NaN: where tiles lie on the
+// mask's edge, such values are taken out on their way to shared memory, and a
+// loop adds them to the rows that see them (`add_special`).
 #include <hip/hip_runtime.h>
 
 #include "cache_internal.h"
@@ -53,6 +54,12 @@ struct Held {
     typedef Bf16 V;
     static __device__ __forceinline__ u32x4 key(piece p) { return Widen<T, F>::eight(p); }
     static __device__ __forceinline__ u32x4 value(piece p) { return Widen<Bf16, F>::eight(p); }
+    // four values as two words of V
+    static __device__ __forceinline__ u32x2 value4(const uint8_t *p)
+    {
+        const u32x4 w = Widen<Bf16, F>::eight(u32x2{*(const uint32_t *)p, 0});
+        return u32x2{w.x, w.y};
+    }
 };
 template <class T>
 struct Held<T, void> {
@@ -61,6 +68,7 @@ struct Held<T, void> {
     typedef T V;
     static __device__ __forceinline__ u32x4 key(piece p) { return p; }
     static __device__ __forceinline__ u32x4 value(piece p) { return p; }
+    static __device__ __forceinline__ u32x2 value4(const uint8_t *p) { return *(const u32x2 *)p; }
 };
 
 // Lanes 0-31 and 32-63 exchange.
@@ -80,45 +88,31 @@ __device__ __forceinline__ u32x4 columns(const uint8_t *at, int second)
     return u32x4{a.x, a.y, b.x, b.y};
 }
 
-// Whether any of eight 16-bit values is an infinity or a NaN.
+// Takes infinities and NaN out of eight 16-bit values; whether there were any.
 template <class T>
-__device__ __forceinline__ bool any_special(u32x4 p)
+__device__ __forceinline__ bool clean(u32x4 &p)
 {
-    bool r = false;
+    bool any = false;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        r |= (p[i] & T::kExponent) == T::kExponent || (p[i] >> 16 & T::kExponent) == T::kExponent;
-    return r;
+    for (int i = 0; i < 4; ++i) {
+        const bool lo = (p[i] & T::kExponent) == T::kExponent;
+        const bool hi = (p[i] >> 16 & T::kExponent) == T::kExponent;
+        p[i] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0x0000ffffu : ~0u);
+        any |= lo || hi;
+    }
+    return any;
 }
 
-// Eight values with infinities and NaN taken out (`clean`), and marks in their
-// place: 1 for +infinity, 1/256 for -infinity, 256 for NaN.  A sum of up to 64
-// marks says which of them there were.
-template <class T>
-__device__ __forceinline__ void part_special(u32x4 p, u32x4 &clean, u32x4 &marks)
+// Adds the infinities and NaN among four values of a row that is seen.
+template <class H>
+__device__ __forceinline__ void add_special(const uint8_t *at, bool sees, float *o)
 {
-    float m[8];
+    const u32x2 w = H::value4(at);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t h = p[i / 2] >> (16 * (i % 2)) & 0xffffu;
-        const bool special = (h & T::kExponent) == T::kExponent;
-        const bool nan = special && (h & ((T::kExponent & (0u - T::kExponent)) - 1));
-        m[i] = !special ? 0.0f : nan ? 256.0f : h & 0x8000u ? 1.0f / 256 : 1.0f;
-        if (special)
-            p[i / 2] &= i % 2 ? 0x0000ffffu : 0xffff0000u;
+    for (int j = 0; j < 4; ++j) {
+        const float x = (float)__builtin_bit_cast(typename H::V::elem, (uint16_t)(w[j / 2] >> (16 * (j % 2))));
+        o[j] += sees && !__builtin_isfinite(x) ? x : 0.0f;
     }
-    clean = p;
-    marks = pack8<T>(m);
-}
-__device__ __forceinline__ float special_of(float marks)
-{
-    const float nan = __builtin_floorf(marks * (1.0f / 256));
-    marks -= nan * 256.0f;
-    const float up = __builtin_floorf(marks);
-    const bool down = marks - up > 0.0f;
-    if (nan > 0.0f || (up > 0.0f && down))
-        return __builtin_nanf("");
-    return up > 0.0f ? __builtin_inff() : down ? -__builtin_inff() : 0.0f;
 }
 
 // The sequence of this workgroup: its query rows and keys, bounded by what the
@@ -167,7 +161,12 @@ __device__ __forceinline__ Place place_of(const AttentionArgs &a, const int32_t 
     return p;
 }
 
-// Where row r's results go; used by both kernels.
+__device__ __forceinline__ uint32_t page_of(const AttentionArgs &a, const int32_t *table, int32_t t, int32_t end)
+{
+    return place_of(a, table, t, end).page;
+}
+
+// Four results of a row, as consecutive 16-bit values.
 template <class T>
 __device__ __forceinline__ void store4(typename T::elem *out, const float *x)
 {
@@ -202,7 +201,7 @@ struct TileShape {
 };
 
 template <class T, class F, int DP>
-__global__ __launch_bounds__(64 * kTileWaves, 2) void kvcache_attention_tile_kernel(const AttentionArgs a)
+__global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void kvcache_attention_tile_kernel(const AttentionArgs a)
 {
     typedef TileShape<DP> S;
     typedef Held<T, F> H;
@@ -270,66 +269,90 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void kvcache_attention_tile_ker
     const uint32_t esize = H::coded ? 1 : 2;
     const uint8_t *kbase = (const uint8_t *)a.k + ((int64_t)head * a.k_head + piece * 8) * esize;
     const uint8_t *vbase = (const uint8_t *)a.v + ((int64_t)head * a.v_head + piece * 8) * esize;
-    Place at[S::kPasses], scale_at;
-    Piece kp[S::kPasses], vp[S::kPasses];
-    float ks = 0.0f, vs = 0.0f;
+    uint32_t page_at[S::kPasses], scale_page = ~0u;
+    Piece next[S::kPasses];
+    float scale_next = 0.0f;
 
     auto look_up = [&](int32_t t0) {
 #pragma unroll
         for (int i = 0; i < S::kPasses; ++i)
-            at[i] = place_of(a, table, t0 + (int32_t)key0 + i * S::kRowsAtOnce, hi);
+            page_at[i] = page_of(a, table, t0 + (int32_t)key0 + i * S::kRowsAtOnce, hi);
         if (H::coded && tid < S::kKeys)
-            scale_at = place_of(a, table, t0 + (int32_t)tid, hi);
+            scale_page = page_of(a, table, t0 + (int32_t)tid, hi);
     };
-    auto load = [&]() {
+    auto load = [&](int32_t t0, const uint8_t *base, int64_t page, int64_t place, const float *scales,
+                    int64_t s_page, int64_t s_place, int64_t s_head) {
 #pragma unroll
         for (int i = 0; i < S::kPasses; ++i) {
-            kp[i] = Piece{};
-            vp[i] = Piece{};
-            if (in && at[i].page != ~0u) {
-                kp[i] = *(const Piece *)(kbase + page_offset(at[i].page, at[i].place, a.k_page, a.k_place) * esize);
-                vp[i] = *(const Piece *)(vbase + page_offset(at[i].page, at[i].place, a.v_page, a.v_place) * esize);
-            }
+            next[i] = Piece{};
+            const uint32_t t = (uint32_t)(t0 + (int32_t)key0 + i * S::kRowsAtOnce);
+            if (in && page_at[i] != ~0u)
+                next[i] = *(const Piece *)(base + page_offset(page_at[i], a.page_size.mod(t, a.page_size.div(t)),
+                                                              page, place) * esize);
         }
         if (H::coded && tid < S::kKeys) {
-            ks = vs = 0.0f;
-            if (scale_at.page != ~0u) {
-                ks = a.k_scale[page_offset(scale_at.page, scale_at.place, a.ks_page, a.ks_place) + head * a.ks_head];
-                vs = a.v_scale[page_offset(scale_at.page, scale_at.place, a.vs_page, a.vs_place) + head * a.vs_head];
-            }
+            scale_next = 0.0f;
+            const uint32_t t = (uint32_t)t0 + tid;
+            if (scale_page != ~0u)
+                scale_next = scales[page_offset(scale_page, a.page_size.mod(t, a.page_size.div(t)), s_page, s_place) +
+                                    head * s_head];
         }
     };
-    auto put = [&](uint8_t *buf) {
+    auto load_keys = [&](int32_t t0) {
+        load(t0, kbase, a.k_page, a.k_place, a.k_scale, a.ks_page, a.ks_place, a.ks_head);
+    };
+    auto load_values = [&](int32_t t0) {
+        load(t0, vbase, a.v_page, a.v_place, a.v_scale, a.vs_page, a.vs_place, a.vs_head);
+    };
+    auto put_keys = [&](uint8_t *buf) {
+#pragma unroll
+        for (int i = 0; i < S::kPasses; ++i)
+            *(u32x4 *)(buf + (key0 + i * S::kRowsAtOnce) * S::kKStride + piece * 16) = H::key(next[i]);
+        if (H::coded && tid < S::kKeys)
+            ((float *)(buf + S::kKBytes + S::kVBytes))[tid] = scale_next;
+    };
+    // whether infinities or NaN were taken out (on the mask's edge only)
+    auto put_values = [&](uint8_t *buf, bool edge) {
+        bool special = false;
 #pragma unroll
         for (int i = 0; i < S::kPasses; ++i) {
-            const uint32_t key = key0 + i * S::kRowsAtOnce;
-            *(u32x4 *)(buf + key * S::kKStride + piece * 16) = H::key(kp[i]);
-            *(u32x4 *)(buf + S::kKBytes + key * S::kVStride + piece * 16) = H::value(vp[i]);
+            u32x4 w = H::value(next[i]);
+            if (edge)
+                special |= clean<V>(w);
+            *(u32x4 *)(buf + S::kKBytes + (key0 + i * S::kRowsAtOnce) * S::kVStride + piece * 16) = w;
         }
-        if (H::coded && tid < S::kKeys) {
-            ((float *)(buf + S::kKBytes + S::kVBytes))[tid] = ks;
-            ((float *)(buf + S::kKBytes + S::kVBytes))[S::kKeys + tid] = vs;
-        }
+        if (H::coded && tid < S::kKeys)
+            ((float *)(buf + S::kKBytes + S::kVBytes))[S::kKeys + tid] = scale_next;
+        return special;
     };
+    // not every row sees every key of the tile
+    auto on_edge = [&](int32_t t0) {
+        return t0 + S::kKeys - 1 > first || t0 + S::kKeys > hi || (a.window > 0 && t0 <= last - a.window);
+    };
+    bool edge = on_edge(lo), special = false;
 
     if (lo < hi) {
         look_up(lo);
-        load();
+        load_keys(lo);
+        put_keys(lds);
+        load_values(lo);
+        special = put_values(lds, edge);
         look_up(lo + S::kKeys);
-        put(lds);
     }
-    __syncthreads();
+    special = __syncthreads_or(special);
 
+    // a row sees key t0 + x if x - see_from is below see_count, unsigned
+    const uint32_t see_count = see_hi < see_lo ? 0 : (uint32_t)(see_hi - see_lo) + 1;
     uint32_t turn = 0;
     for (int32_t t0 = lo; t0 < hi; t0 += S::kKeys, turn ^= 1) {
         const uint8_t *buf = lds + turn * S::kBuffer;
+        uint8_t *other = lds + (turn ^ 1) * S::kBuffer;
         const bool more = t0 + S::kKeys < hi;
-        if (more) {
-            load();
-            look_up(t0 + 2 * S::kKeys);
-        }
+        if (more)
+            load_keys(t0 + S::kKeys);
         const float *kscale = (const float *)(buf + S::kKBytes + S::kVBytes);
         const float *vscale = kscale + S::kKeys;
+        const uint32_t see = (uint32_t)(t0 + (int32_t)half * 4 - see_lo);
 
         // scores
         f32x16 s[S::kKeys / 32];
@@ -353,17 +376,12 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void kvcache_attention_tile_ker
                         s[b][4 * i + j] *= c[j];
                 }
         }
-        // not every row sees every key
-        const bool edge = t0 + S::kKeys - 1 > first || t0 + S::kKeys > hi ||
-                          (a.window > 0 && t0 <= last - a.window);
         if (edge) {
 #pragma unroll
             for (int b = 0; b < S::kKeys / 32; ++b)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int32_t t = t0 + b * 32 + (i / 4) * 8 + (int32_t)half * 4 + i % 4;
-                    s[b][i] = t <= see_hi && t >= see_lo ? s[b][i] : -__builtin_inff();
-                }
+                for (int i = 0; i < 16; ++i)
+                    s[b][i] = see + (b * 32 + (i / 4) * 8 + i % 4) < see_count ? s[b][i] : -__builtin_inff();
         }
 
         // the running maximum, in units of log2
@@ -398,67 +416,65 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void kvcache_attention_tile_ker
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const f32x4 c = *(const f32x4 *)(vscale + b * 32 + i * 8 + half * 4);
+                    // a hidden row's scale may be anything
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float y = w[4 * i + j] * c[j];
-                        // a hidden row's scale may be anything
-                        w[4 * i + j] = edge && s[b][4 * i + j] == -__builtin_inff() ? 0.0f : y;
-                    }
+                    for (int j = 0; j < 4; ++j)
+                        w[4 * i + j] = w[4 * i + j] == 0.0f ? 0.0f : w[4 * i + j] * c[j];
                 }
             }
             p[2 * b] = __builtin_bit_cast(typename V::eight, pack8<V>(w));
             p[2 * b + 1] = __builtin_bit_cast(typename V::eight, pack8<V>(w + 8));
         }
+        __builtin_amdgcn_sched_barrier(0);
+        if (more) {
+            put_keys(other);
+            load_values(t0 + S::kKeys);
+            look_up(t0 + 2 * S::kKeys);
+        }
 
         // values: of a block of 16 keys, p holds keys 4 half .. + 3 and 8 + 4 half .. + 3
         const uint8_t *vat = buf + S::kKBytes + (half * 4 + (lane % 16) / 4) * S::kVStride +
                              ((lane / 16) % 2) * 32 + (lane % 4) * 8;
-        bool special = false;
-        if (edge) {
+#pragma unroll
+        for (int i = 0; i < S::kKeys / 16; ++i)
+#pragma unroll
+            for (int d = 0; d < DP / 32; ++d)
+                o[d] = V::mfma32(__builtin_bit_cast(typename V::eight,
+                                                    columns(vat + i * 16 * S::kVStride + d * 64, 8 * S::kVStride)),
+                                 p[i], o[d]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (special) {
 #pragma unroll 1
-            for (int i = 0; i < S::kKeys / 16; ++i)
+            for (int32_t t = t0; t < t0 + S::kKeys && t < hi; ++t) {
+                const Place from = place_of(a, table, t, hi);
+                if (from.page == ~0u)
+                    continue;
+                const bool sees = (uint32_t)(t - see_lo) < see_count;
+                const uint8_t *at_v = (const uint8_t *)a.v + ((int64_t)head * a.v_head + half * 4 +
+                                      page_offset(from.page, from.place, a.v_page, a.v_place)) * esize;
 #pragma unroll
                 for (int d = 0; d < DP / 32; ++d)
-                    special |= any_special<V>(columns(vat + i * 16 * S::kVStride + d * 64, 8 * S::kVStride));
-            special = __builtin_amdgcn_ballot_w64(special) != 0;
-        }
-        if (!special) {
 #pragma unroll
-            for (int i = 0; i < S::kKeys / 16; ++i)
+                    for (int i = 0; i < 4; ++i) {
+                        float x[4] = {};
+                        if (d * 32 + i * 8 + half * 4 < a.head_dim)
+                            add_special<H>(at_v + (d * 32 + i * 8) * esize, sees, x);
 #pragma unroll
-                for (int d = 0; d < DP / 32; ++d)
-                    o[d] = V::mfma32(__builtin_bit_cast(typename V::eight,
-                                                        columns(vat + i * 16 * S::kVStride + d * 64, 8 * S::kVStride)),
-                                     p[i], o[d]);
-        } else {
-            // infinities and NaN among the values: the finite ones as above,
-            // and for the others a count, with weight 1 for keys that are seen
-#pragma unroll
-            for (int d = 0; d < DP / 32; ++d) {
-                f32x16 marks = {};
-#pragma unroll
-                for (int i = 0; i < S::kKeys / 16; ++i) {
-                    u32x4 clean, mark;
-                    part_special<V>(columns(vat + i * 16 * S::kVStride + d * 64, 8 * S::kVStride), clean, mark);
-                    float one[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int32_t t = t0 + i * 16 + (j / 4) * 8 + (int32_t)half * 4 + j % 4;
-                        one[j] = t <= see_hi && t >= see_lo ? 1.0f : 0.0f;
+                        for (int j = 0; j < 4; ++j)
+                            o[d][4 * i + j] += x[j];
+                        __builtin_amdgcn_sched_barrier(0);
                     }
-                    o[d] = V::mfma32(__builtin_bit_cast(typename V::eight, clean), p[i], o[d]);
-                    marks = V::mfma32(__builtin_bit_cast(typename V::eight, mark),
-                                      __builtin_bit_cast(typename V::eight, pack8<V>(one)), marks);
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    o[d][i] += special_of(marks[i]);
             }
         }
 
-        if (more)
-            put(lds + (turn ^ 1) * S::kBuffer);
-        __syncthreads();
+        if (more) {
+            edge = on_edge(t0 + S::kKeys);
+            special = put_values(other, edge);
+        }
+        if (edge)
+            special = __syncthreads_or(special);
+        else
+            __syncthreads();
     }
 
     l += other_half(l);
@@ -641,9 +657,17 @@ __global__ __launch_bounds__(64 * kSingleWaves) void kvcache_attention_single_ke
             scales[lane] = ks;
             scales[32 + lane] = vs;
         }
+        // not every row sees every key
+        const bool edge = t0 + kSingleKeys - 1 > first || t0 + kSingleKeys > hi ||
+                          (a.window > 0 && t0 <= last - a.window);
+        bool special = false;
 #pragma unroll
-        for (int i = 0; i < S::kPasses; ++i)
-            *(u32x4 *)(vlds + (i * S::kRowsAtOnce + vkey) * S::kVStride + piece * 16) = H::value(vp[i]);
+        for (int i = 0; i < S::kPasses; ++i) {
+            u32x4 w = H::value(vp[i]);
+            if (edge)
+                special |= clean<V>(w);
+            *(u32x4 *)(vlds + (i * S::kRowsAtOnce + vkey) * S::kVStride + piece * 16) = w;
+        }
         // the wavefront's own writes, read back by other lanes of it: in order
         // in the LDS queue, and kept in order by the compiler
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -661,8 +685,6 @@ __global__ __launch_bounds__(64 * kSingleWaves) void kvcache_attention_single_ke
                 vscale[b] = *(const f32x4 *)(scales + 32 + b * 16 + group * 4);
             }
         }
-        const bool edge = t0 + kSingleKeys - 1 > first || t0 + kSingleKeys > hi ||
-                          (a.window > 0 && t0 <= last - a.window);
         if (edge) {
 #pragma unroll
             for (int b = 0; b < 2; ++b)
@@ -699,41 +721,32 @@ __global__ __launch_bounds__(64 * kSingleWaves) void kvcache_attention_single_ke
                 l += w[4 * b + j];
                 if (H::coded) {
                     const float y = w[4 * b + j] * vscale[b][j];
-                    w[4 * b + j] = edge && s[b][j] == -__builtin_inff() ? 0.0f : y;
+                    w[4 * b + j] = w[4 * b + j] == 0.0f ? 0.0f : y;
                 }
             }
         const typename V::eight p = __builtin_bit_cast(typename V::eight, pack8<V>(w));
 
         // keys 4 group .. + 3 and 16 + 4 group .. + 3, columns 16 d + lane % 16
         const uint8_t *vat = vlds + (group * 4 + col / 4) * S::kVStride + (col % 4) * 8;
-        bool special = false;
-        if (edge) {
 #pragma unroll
-            for (int d = 0; d < DP / 16; ++d)
-                special |= any_special<V>(columns(vat + d * 32, 16 * S::kVStride));
-            special = __builtin_amdgcn_ballot_w64(special) != 0;
-        }
-        if (!special) {
+        for (int d = 0; d < DP / 16; ++d)
+            o[d] = V::mfma16(__builtin_bit_cast(typename V::eight, columns(vat + d * 32, 16 * S::kVStride)), p, o[d]);
+        if (__builtin_amdgcn_ballot_w64(special)) {
+#pragma unroll 1
+            for (int32_t t = t0; t < t0 + kSingleKeys && t < hi; ++t) {
+                const Place from = place_of(a, table, t, hi);
+                if (from.page == ~0u)
+                    continue;
+                const uint8_t *at_v = (const uint8_t *)a.v + ((int64_t)head * a.v_head + group * 4 +
+                                      page_offset(from.page, from.place, a.v_page, a.v_place)) * esize;
 #pragma unroll
-            for (int d = 0; d < DP / 16; ++d)
-                o[d] = V::mfma16(__builtin_bit_cast(typename V::eight, columns(vat + d * 32, 16 * S::kVStride)), p, o[d]);
-        } else {
-            float one[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int32_t t = t0 + (j / 4) * 16 + (int32_t)group * 4 + j % 4;
-                one[j] = t <= see_hi && t >= see_lo ? 1.0f : 0.0f;
-            }
-            const typename V::eight ones = __builtin_bit_cast(typename V::eight, pack8<V>(one));
-#pragma unroll
-            for (int d = 0; d < DP / 16; ++d) {
-                u32x4 clean, mark;
-                part_special<V>(columns(vat + d * 32, 16 * S::kVStride), clean, mark);
-                o[d] = V::mfma16(__builtin_bit_cast(typename V::eight, clean), p, o[d]);
-                const f32x4 marks = V::mfma16(__builtin_bit_cast(typename V::eight, mark), ones, f32x4{});
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    o[d][j] += special_of(marks[j]);
+                for (int d = 0; d < DP / 16; ++d) {
+                    float x[4] = {};
+                    if (d * 16 + group * 4 < a.head_dim)
+                        add_special<H>(at_v + d * 16 * esize, t <= see_hi && t >= see_lo, x);
+                    o[d] += f32x4{x[0], x[1], x[2], x[3]};
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
         }
         // the next step's writes stay behind these reads
