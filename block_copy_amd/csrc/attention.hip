@@ -40,6 +40,7 @@ constexpr int kTileRows = 32 * kTileWaves;
 constexpr int kSingleWaves = 4;   // of the kernel for few rows: each its own keys
 constexpr int kSingleRows = 16;
 constexpr int kSingleKeys = 32;   // keys of a wavefront's step
+constexpr int kMaxRowBytes = KVCACHE_MAX_ATTENTION_HEAD_DIM * 2;
 
 typedef int16_t i16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
@@ -87,6 +88,47 @@ __device__ __forceinline__ u32x4 columns(const uint8_t *at, int second)
     const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(at + second)));
     return u32x4{a.x, a.y, b.x, b.y};
 }
+
+// Where reads of shared memory and products stay on their side (vector and
+// scalar arithmetic may pass).  Left alone, the compiler sinks each read to
+// its product and waits there.
+__device__ __forceinline__ void keep_order()
+{
+    __builtin_amdgcn_sched_barrier(0x2 | 0x4 | 0x400);
+}
+
+// N products in order, the operands of each read four products ahead: read(n)
+// gives product n's, use(n, operand) takes it.  The first four may come from
+// an earlier `begin`.
+template <class E, int N>
+struct Feed {
+    E f[2][4];
+    template <class Read>
+    __device__ __forceinline__ void begin(Read &&read)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            f[0][i] = read(i);
+        keep_order();
+    }
+    template <class Read, class Use>
+    __device__ __forceinline__ void run(Read &&read, Use &&use)
+    {
+#pragma unroll
+        for (int g = 0; g < N / 4; ++g) {
+            if (g + 1 < N / 4) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    f[(g + 1) & 1][i] = read(4 * (g + 1) + i);
+            }
+            keep_order();
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                use(4 * g + i, f[g & 1][i]);
+            keep_order();
+        }
+    }
+};
 
 // Takes infinities and NaN out of eight 16-bit values; whether there were any.
 template <class T>
@@ -140,30 +182,44 @@ __device__ __forceinline__ Sequence sequence_of(const AttentionArgs &a, uint32_t
     return r;
 }
 
-// The page and place of token t, or a page of ~0 for one that reads as zeros.
-struct Place {
-    uint32_t page, place;
-};
-__device__ __forceinline__ Place place_of(const AttentionArgs &a, const int32_t *table, int32_t t, int32_t end)
-{
-    Place p;
-    p.page = ~0u;
-    p.place = 0;
-    if (t < end) {
-        const uint32_t column = a.page_size.div((uint32_t)t);
-        p.place = a.page_size.mod((uint32_t)t, column);
-        p.page = (uint32_t)table[column];
-        if (p.page >= a.num_pages) {
-            set_status(a.status, KVCACHE_BAD_PAGE);
-            p.page = ~0u;
-        }
-    }
-    return p;
-}
+// Where rows that read as zeros are read: those past a sequence's keys, and of
+// page numbers out of range.  (An address picked costs less than a branch
+// around each read.)
+static __device__ const u32x4 kZeros[kMaxRowBytes / 16] = {};
 
+// The page of token t < end; ~0 from `end` on, and for a number out of range.
 __device__ __forceinline__ uint32_t page_of(const AttentionArgs &a, const int32_t *table, int32_t t, int32_t end)
 {
-    return place_of(a, table, t, end).page;
+    uint32_t page = ~0u;
+    if (t < end) {
+        page = (uint32_t)table[a.page_size.div((uint32_t)t)];
+        if (page >= a.num_pages) {
+            set_status(a.status, KVCACHE_BAD_PAGE);
+            page = ~0u;
+        }
+    }
+    return page;
+}
+
+// Token t's place in `page`, by an array's strides.
+__device__ __forceinline__ int64_t offset_in(const AttentionArgs &a, uint32_t page, int32_t t, int64_t page_stride,
+                                             int64_t place_stride)
+{
+    return page_offset(page, a.page_size.mod((uint32_t)t, a.page_size.div((uint32_t)t)), page_stride, place_stride);
+}
+
+__device__ __forceinline__ uint64_t row_address(const AttentionArgs &a, uint32_t page, int32_t t, const uint8_t *base,
+                                                int64_t page_stride, int64_t place_stride, uint32_t esize)
+{
+    return page == ~0u ? (uint64_t)kZeros
+                       : (uint64_t)base + offset_in(a, page, t, page_stride, place_stride) * esize;
+}
+
+// A piece at an address that came out of shared memory: global, not flat.
+template <class P>
+__device__ __forceinline__ P load_at(uint64_t address)
+{
+    return *(const __attribute__((address_space(1))) P *)address;
 }
 
 // Four results of a row, as consecutive 16-bit values.
@@ -182,7 +238,10 @@ __device__ __forceinline__ void store4(typename T::elem *out, const float *x)
 // and walks the keys in tiles of Keys, all wavefronts reading the same tile
 // from shared memory.  The next tile's rows are in flight to registers while a
 // tile is worked on, and go to the other shared buffer at its end: one barrier
-// a tile.  Rows of shared memory are padded so that neither the 16-byte reads
+// a tile.  Their addresses come from a table in shared memory, which two
+// wavefronts fill a tile ahead, one key a lane (the other two fetch an 8-bit
+// format's scales): worked out by every thread for its own pieces they took
+// more vector instructions than the softmax.  Rows of shared memory are padded so that neither the 16-byte reads
 // of K (stride = 16 bytes mod 256) nor the transposing reads of V (64 mod 256)
 // meet in a bank.
 
@@ -194,7 +253,8 @@ struct TileShape {
     static constexpr int kKBytes = kKeys * kKStride;
     static constexpr int kVBytes = kKeys * kVStride;
     static constexpr int kScaleBytes = kKeys * 8;
-    static constexpr int kBuffer = kKBytes + kVBytes + kScaleBytes;
+    static constexpr int kTableBytes = kKeys * 16;                        // addresses of the rows of K and V
+    static constexpr int kBuffer = kKBytes + kVBytes + kScaleBytes + kTableBytes;
     static constexpr int kPieces = DP / 8;                                // of a row
     static constexpr int kRowsAtOnce = 64 * kTileWaves / kPieces;
     static constexpr int kPasses = kKeys / kRowsAtOnce;
@@ -267,49 +327,50 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void kvcache_at
     const uint32_t piece = tid % S::kPieces, key0 = tid / S::kPieces;
     const bool in = piece * 8 < a.head_dim;
     const uint32_t esize = H::coded ? 1 : 2;
-    const uint8_t *kbase = (const uint8_t *)a.k + ((int64_t)head * a.k_head + piece * 8) * esize;
-    const uint8_t *vbase = (const uint8_t *)a.v + ((int64_t)head * a.v_head + piece * 8) * esize;
-    uint32_t page_at[S::kPasses], scale_page = ~0u;
     Piece next[S::kPasses];
-    float scale_next = 0.0f;
+    // of key `lane` of the tile after next, later of the next one
+    uint32_t page = ~0u;
+    float scale = 0.0f;
 
+    auto table_of = [&](uint8_t *buf) { return (uint64_t *)(buf + S::kKBytes + S::kVBytes + S::kScaleBytes); };
+    auto scales_of = [&](uint8_t *buf) { return (float *)(buf + S::kKBytes + S::kVBytes); };
     auto look_up = [&](int32_t t0) {
-#pragma unroll
-        for (int i = 0; i < S::kPasses; ++i)
-            page_at[i] = page_of(a, table, t0 + (int32_t)key0 + i * S::kRowsAtOnce, hi);
-        if (H::coded && tid < S::kKeys)
-            scale_page = page_of(a, table, t0 + (int32_t)tid, hi);
+        page = ~0u;
+        if (lane < S::kKeys && (H::coded || wave < 2))
+            page = page_of(a, table, t0 + (int32_t)lane, hi);
     };
-    auto load = [&](int32_t t0, const uint8_t *base, int64_t page, int64_t place, const float *scales,
-                    int64_t s_page, int64_t s_place, int64_t s_head) {
+    auto put_table = [&](uint8_t *buf, int32_t t0) {
+        const int32_t t = t0 + (int32_t)lane;
+        if (wave == 0 && lane < S::kKeys)
+            table_of(buf)[lane] = row_address(a, page, t, (const uint8_t *)a.k + (int64_t)head * a.k_head * esize,
+                                              a.k_page, a.k_place, esize);
+        if (wave == 1 && lane < S::kKeys)
+            table_of(buf)[S::kKeys + lane] =
+                row_address(a, page, t, (const uint8_t *)a.v + (int64_t)head * a.v_head * esize, a.v_page, a.v_place, esize);
+    };
+    auto load_scales = [&](int32_t t0) {
+        if (H::coded && wave >= 2) {
+            scale = 0.0f;
+            if (page != ~0u)
+                scale = wave == 2 ? a.k_scale[offset_in(a, page, t0 + (int32_t)lane, a.ks_page, a.ks_place) + head * a.ks_head]
+                                  : a.v_scale[offset_in(a, page, t0 + (int32_t)lane, a.vs_page, a.vs_place) + head * a.vs_head];
+        }
+    };
+    auto put_scales = [&](uint8_t *buf) {
+        if (H::coded && wave >= 2 && lane < S::kKeys)
+            scales_of(buf)[(wave - 2) * S::kKeys + lane] = scale;
+    };
+    auto load = [&](const uint64_t *addresses) {
 #pragma unroll
         for (int i = 0; i < S::kPasses; ++i) {
-            next[i] = Piece{};
-            const uint32_t t = (uint32_t)(t0 + (int32_t)key0 + i * S::kRowsAtOnce);
-            if (in && page_at[i] != ~0u)
-                next[i] = *(const Piece *)(base + page_offset(page_at[i], a.page_size.mod(t, a.page_size.div(t)),
-                                                              page, place) * esize);
+            const uint64_t at = addresses[key0 + i * S::kRowsAtOnce] + piece * 8 * esize;
+            next[i] = load_at<Piece>(in ? at : (uint64_t)kZeros);
         }
-        if (H::coded && tid < S::kKeys) {
-            scale_next = 0.0f;
-            const uint32_t t = (uint32_t)t0 + tid;
-            if (scale_page != ~0u)
-                scale_next = scales[page_offset(scale_page, a.page_size.mod(t, a.page_size.div(t)), s_page, s_place) +
-                                    head * s_head];
-        }
-    };
-    auto load_keys = [&](int32_t t0) {
-        load(t0, kbase, a.k_page, a.k_place, a.k_scale, a.ks_page, a.ks_place, a.ks_head);
-    };
-    auto load_values = [&](int32_t t0) {
-        load(t0, vbase, a.v_page, a.v_place, a.v_scale, a.vs_page, a.vs_place, a.vs_head);
     };
     auto put_keys = [&](uint8_t *buf) {
 #pragma unroll
         for (int i = 0; i < S::kPasses; ++i)
             *(u32x4 *)(buf + (key0 + i * S::kRowsAtOnce) * S::kKStride + piece * 16) = H::key(next[i]);
-        if (H::coded && tid < S::kKeys)
-            ((float *)(buf + S::kKBytes + S::kVBytes))[tid] = scale_next;
     };
     // whether infinities or NaN were taken out (on the mask's edge only)
     auto put_values = [&](uint8_t *buf, bool edge) {
@@ -321,8 +382,6 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void kvcache_at
                 special |= clean<V>(w);
             *(u32x4 *)(buf + S::kKBytes + (key0 + i * S::kRowsAtOnce) * S::kVStride + piece * 16) = w;
         }
-        if (H::coded && tid < S::kKeys)
-            ((float *)(buf + S::kKBytes + S::kVBytes))[S::kKeys + tid] = scale_next;
         return special;
     };
     // not every row sees every key of the tile
@@ -331,13 +390,19 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void kvcache_at
     };
     bool edge = on_edge(lo), special = false;
 
+    // the first tile, and the table of the second
     if (lo < hi) {
         look_up(lo);
-        load_keys(lo);
-        put_keys(lds);
-        load_values(lo);
-        special = put_values(lds, edge);
+        put_table(lds, lo);
+        load_scales(lo);
+        put_scales(lds);
         look_up(lo + S::kKeys);
+        put_table(lds + S::kBuffer, lo + S::kKeys);
+        __syncthreads();
+        load(table_of(lds));
+        put_keys(lds);
+        load(table_of(lds) + S::kKeys);
+        special = put_values(lds, edge);
     }
     special = __syncthreads_or(special);
 
@@ -345,25 +410,38 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void kvcache_at
     const uint32_t see_count = see_hi < see_lo ? 0 : (uint32_t)(see_hi - see_lo) + 1;
     uint32_t turn = 0;
     for (int32_t t0 = lo; t0 < hi; t0 += S::kKeys, turn ^= 1) {
-        const uint8_t *buf = lds + turn * S::kBuffer;
-        uint8_t *other = lds + (turn ^ 1) * S::kBuffer;
+        uint8_t *buf = lds + turn * S::kBuffer, *other = lds + (turn ^ 1) * S::kBuffer;
         const bool more = t0 + S::kKeys < hi;
-        if (more)
-            load_keys(t0 + S::kKeys);
-        const float *kscale = (const float *)(buf + S::kKBytes + S::kVBytes);
-        const float *vscale = kscale + S::kKeys;
+        if (more) {
+            load(table_of(other));
+            load_scales(t0 + S::kKeys);
+            look_up(t0 + 2 * S::kKeys);
+        }
+        const float *kscale = scales_of(buf), *vscale = kscale + S::kKeys;
         const uint32_t see = (uint32_t)(t0 + (int32_t)half * 4 - see_lo);
 
         // scores
         f32x16 s[S::kKeys / 32];
-#pragma unroll
-        for (int b = 0; b < S::kKeys / 32; ++b) {
-            s[b] = f32x16{};
-            const uint8_t *kat = buf + (b * 32 + col) * S::kKStride + half * 16;
-#pragma unroll
-            for (int i = 0; i < DP / 16; ++i)
-                s[b] = T::mfma32(*(const typename T::eight *)(kat + i * 32), q[i], s[b]);
-        }
+        const uint8_t *kat = buf + col * S::kKStride + half * 16;
+        constexpr int kBlocks = S::kKeys / 32;
+        const auto read_k = [&](int n) {
+            return *(const typename T::eight *)(kat + n % kBlocks * 32 * S::kKStride + n / kBlocks * 32);
+        };
+        Feed<typename T::eight, kBlocks * DP / 16> k_feed;
+        k_feed.begin(read_k);
+        k_feed.run(read_k, [&](int n, typename T::eight k) {
+            const int b = n % kBlocks, i = n / kBlocks;
+            s[b] = T::mfma32(k, q[i], i == 0 ? f32x16{} : s[b]);
+        });
+        // values: of a block of 16 keys, keys 4 half .. + 3 and 8 + 4 half .. + 3
+        const uint8_t *vat = buf + S::kKBytes + (half * 4 + (lane % 16) / 4) * S::kVStride +
+                             ((lane / 16) % 2) * 32 + (lane % 4) * 8;
+        const auto read_v = [&](int n) {
+            return __builtin_bit_cast(typename V::eight, columns(vat + n / (DP / 32) * 16 * S::kVStride +
+                                                                 n % (DP / 32) * 64, 8 * S::kVStride));
+        };
+        Feed<typename V::eight, S::kKeys / 16 * DP / 32> v_feed;
+        v_feed.begin(read_v);
         // register 4 i + j of block b is key t0 + 32 b + 8 i + 4 half + j
         if (H::coded) {
 #pragma unroll
@@ -428,30 +506,22 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void kvcache_at
         __builtin_amdgcn_sched_barrier(0);
         if (more) {
             put_keys(other);
-            load_values(t0 + S::kKeys);
-            look_up(t0 + 2 * S::kKeys);
+            load(table_of(other) + S::kKeys);
         }
 
-        // values: of a block of 16 keys, p holds keys 4 half .. + 3 and 8 + 4 half .. + 3
-        const uint8_t *vat = buf + S::kKBytes + (half * 4 + (lane % 16) / 4) * S::kVStride +
-                             ((lane / 16) % 2) * 32 + (lane % 4) * 8;
-#pragma unroll
-        for (int i = 0; i < S::kKeys / 16; ++i)
-#pragma unroll
-            for (int d = 0; d < DP / 32; ++d)
-                o[d] = V::mfma32(__builtin_bit_cast(typename V::eight,
-                                                    columns(vat + i * 16 * S::kVStride + d * 64, 8 * S::kVStride)),
-                                 p[i], o[d]);
+        v_feed.run(read_v, [&](int n, typename V::eight v) {
+            o[n % (DP / 32)] = V::mfma32(v, p[n / (DP / 32)], o[n % (DP / 32)]);
+        });
         __builtin_amdgcn_sched_barrier(0);
         if (special) {
 #pragma unroll 1
             for (int32_t t = t0; t < t0 + S::kKeys && t < hi; ++t) {
-                const Place from = place_of(a, table, t, hi);
-                if (from.page == ~0u)
+                const uint32_t from = page_of(a, table, t, hi);
+                if (from == ~0u)
                     continue;
                 const bool sees = (uint32_t)(t - see_lo) < see_count;
                 const uint8_t *at_v = (const uint8_t *)a.v + ((int64_t)head * a.v_head + half * 4 +
-                                      page_offset(from.page, from.place, a.v_page, a.v_place)) * esize;
+                                      offset_in(a, from, t, a.v_page, a.v_place)) * esize;
 #pragma unroll
                 for (int d = 0; d < DP / 32; ++d)
 #pragma unroll
@@ -470,6 +540,8 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void kvcache_at
         if (more) {
             edge = on_edge(t0 + S::kKeys);
             special = put_values(other, edge);
+            put_scales(other);
+            put_table(buf, t0 + 2 * S::kKeys);   // its rows have been read: by the last barrier
         }
         if (edge)
             special = __syncthreads_or(special);
@@ -531,7 +603,7 @@ template <int DP>
 struct SingleShape {
     static constexpr int kVStride = DP * 2 + 32;   // 32 mod 256: see above, for blocks of 16 rows
     static constexpr int kVBytes = kSingleKeys * kVStride;
-    static constexpr int kWaveBytes = kVBytes + kSingleKeys * 8;   // and the scales
+    static constexpr int kWaveBytes = kVBytes + kSingleKeys * (8 + 16);   // and the scales and addresses
     static constexpr int kPieces = DP / 8;
     static constexpr int kRowsAtOnce = 64 / kPieces;
     static constexpr int kPasses = kSingleKeys / kRowsAtOnce;
@@ -589,74 +661,68 @@ __global__ __launch_bounds__(64 * kSingleWaves) void kvcache_attention_single_ke
     }
 
     uint8_t *vlds = lds + wave * S::kWaveBytes;
-    float *scales = (float *)(vlds + S::kVBytes);   // 32 of the keys, 32 of the values
+    float *scales = (float *)(vlds + S::kVBytes);              // 32 of the keys, 32 of the values
+    uint64_t *addresses = (uint64_t *)(scales + 2 * kSingleKeys);   // likewise
     f32x4 o[DP / 16] = {};
     float m = -__builtin_inff(), l = 0.0f;
 
     const uint32_t esize = H::coded ? 1 : 2;
-    const uint8_t *kbase = (const uint8_t *)a.k + ((int64_t)head * a.k_head + group * 8) * esize;
     const uint32_t piece = lane % S::kPieces, vkey = lane / S::kPieces;
-    const uint8_t *vbase = (const uint8_t *)a.v + ((int64_t)head * a.v_head + piece * 8) * esize;
     const bool vin = piece * 8 < a.head_dim;
     Piece kp[2][DP / 32], vp[S::kPasses];
-    float ks = 0.0f, vs = 0.0f;
-    Place mine;   // lanes 0-31: of key `lane` of the next step
+    // lanes 0-31: of key `lane` of a coming step; 32-63: of value lane - 32
+    uint32_t page;
+    float scale = 0.0f;
+    const uint8_t *base = lane < 32 ? (const uint8_t *)a.k + (int64_t)head * a.k_head * esize
+                                    : (const uint8_t *)a.v + (int64_t)head * a.v_head * esize;
+    const int64_t page_stride = lane < 32 ? a.k_page : a.v_page, place_stride = lane < 32 ? a.k_place : a.v_place;
 
-    auto other = [&](uint32_t key) {
-        Place p;
-        p.page = __shfl(mine.page, key, 64);
-        p.place = __shfl(mine.place, key, 64);
-        return p;
+    auto look_up = [&](int32_t t0) { page = page_of(a, table, t0 + (int32_t)(lane & 31u), hi); };
+    auto put_table = [&](int32_t t0) {
+        const int32_t t = t0 + (int32_t)(lane & 31u);
+        addresses[lane] = row_address(a, page, t, base, page_stride, place_stride, esize);
+        if (H::coded) {
+            scale = 0.0f;
+            if (page != ~0u)
+                scale = lane < 32 ? a.k_scale[offset_in(a, page, t, a.ks_page, a.ks_place) + head * a.ks_head]
+                                  : a.v_scale[offset_in(a, page, t, a.vs_page, a.vs_place) + head * a.vs_head];
+        }
     };
-    auto load_keys = [&]() {
+    auto load_rows = [&]() {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            const Place p = other(b * 16 + col);
-            const uint8_t *at = kbase + page_offset(p.page, p.place, a.k_page, a.k_place) * esize;
+            const uint64_t at = addresses[b * 16 + col] + group * 8 * esize;
 #pragma unroll
-            for (int s = 0; s < DP / 32; ++s) {
-                kp[b][s] = Piece{};
-                if (p.page != ~0u && s * 32 + group * 8 < a.head_dim)
-                    kp[b][s] = *(const Piece *)(at + s * 32 * esize);
-            }
+            for (int s = 0; s < DP / 32; ++s)
+                kp[b][s] = load_at<Piece>(s * 32 + group * 8 < a.head_dim ? at + s * 32 * esize : (uint64_t)kZeros);
         }
-        if (H::coded) {
-            ks = vs = 0.0f;
-            if (lane < 32 && mine.page != ~0u) {
-                ks = a.k_scale[page_offset(mine.page, mine.place, a.ks_page, a.ks_place) + head * a.ks_head];
-                vs = a.v_scale[page_offset(mine.page, mine.place, a.vs_page, a.vs_place) + head * a.vs_head];
-            }
-        }
-    };
-    auto load_values = [&]() {
 #pragma unroll
         for (int i = 0; i < S::kPasses; ++i) {
-            const Place p = other(i * S::kRowsAtOnce + vkey);
-            vp[i] = Piece{};
-            if (vin && p.page != ~0u)
-                vp[i] = *(const Piece *)(vbase + page_offset(p.page, p.place, a.v_page, a.v_place) * esize);
+            const uint64_t at = addresses[kSingleKeys + i * S::kRowsAtOnce + vkey] + piece * 8 * esize;
+            vp[i] = load_at<Piece>(vin ? at : (uint64_t)kZeros);
         }
     };
 
     constexpr int kStep = kSingleKeys * kSingleWaves;
     int32_t t0 = lo + (int32_t)wave * kSingleKeys;
-    mine = place_of(a, table, t0 + (int32_t)(lane & 31u), hi);
-    if (t0 < hi) {
-        load_keys();
-        load_values();
-    }
+    look_up(t0);
+    put_table(t0);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    load_rows();
+    float scale_now = scale;
+    look_up(t0 + kStep);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    put_table(t0 + kStep);
+    look_up(t0 + 2 * kStep);
     for (; t0 < hi; t0 += kStep) {
-        mine = place_of(a, table, t0 + kStep + (int32_t)(lane & 31u), hi);
         f32x4 s[2] = {};
 #pragma unroll
         for (int i = 0; i < DP / 32; ++i)
 #pragma unroll
             for (int b = 0; b < 2; ++b)
                 s[b] = T::mfma16(__builtin_bit_cast(typename T::eight, H::key(kp[b][i])), q[i], s[b]);
-        if (H::coded && lane < 32) {
-            scales[lane] = ks;
-            scales[32 + lane] = vs;
-        }
+        if (H::coded)
+            scales[lane] = scale_now;
         // not every row sees every key
         const bool edge = t0 + kSingleKeys - 1 > first || t0 + kSingleKeys > hi ||
                           (a.window > 0 && t0 <= last - a.window);
@@ -671,10 +737,8 @@ __global__ __launch_bounds__(64 * kSingleWaves) void kvcache_attention_single_ke
         // the wavefront's own writes, read back by other lanes of it: in order
         // in the LDS queue, and kept in order by the compiler
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        if (t0 + kStep < hi) {
-            load_keys();
-            load_values();
-        }
+        scale_now = scale;
+        load_rows();   // of the next step: zeros behind the last key
 
         // register j of block b is key t0 + 16 b + 4 group + j
         f32x4 vscale[2];
@@ -734,11 +798,11 @@ __global__ __launch_bounds__(64 * kSingleWaves) void kvcache_attention_single_ke
         if (__builtin_amdgcn_ballot_w64(special)) {
 #pragma unroll 1
             for (int32_t t = t0; t < t0 + kSingleKeys && t < hi; ++t) {
-                const Place from = place_of(a, table, t, hi);
-                if (from.page == ~0u)
+                const uint32_t from = page_of(a, table, t, hi);
+                if (from == ~0u)
                     continue;
                 const uint8_t *at_v = (const uint8_t *)a.v + ((int64_t)head * a.v_head + group * 4 +
-                                      page_offset(from.page, from.place, a.v_page, a.v_place)) * esize;
+                                      offset_in(a, from, t, a.v_page, a.v_place)) * esize;
 #pragma unroll
                 for (int d = 0; d < DP / 16; ++d) {
                     float x[4] = {};
@@ -751,6 +815,8 @@ __global__ __launch_bounds__(64 * kSingleWaves) void kvcache_attention_single_ke
         }
         // the next step's writes stay behind these reads
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        put_table(t0 + 2 * kStep);
+        look_up(t0 + 3 * kStep);
     }
 
     // join the four wavefronts
@@ -765,10 +831,9 @@ __global__ __launch_bounds__(64 * kSingleWaves) void kvcache_attention_single_ke
 #pragma unroll
     for (int w = 0; w < kSingleWaves; ++w)
         top = __builtin_fmaxf(top, join_m[w][col]);
-    const float base = top == -__builtin_inff() ? 0.0f : top;
     float *joined = (float *)lds;   // [wave][row][DP + 4]
     {
-        const float f = m == top ? 1.0f : __builtin_amdgcn_exp2f(m - base);
+        const float f = m == top ? 1.0f : __builtin_amdgcn_exp2f(m - top);
         float *to = joined + (wave * kSingleRows + col) * (DP + 4);
 #pragma unroll
         for (int d = 0; d < DP / 16; ++d)
