@@ -39,7 +39,6 @@ constexpr int kTileWaves = 4;     // wavefronts of a tile kernel's workgroup, 32
 constexpr int kTileRows = 32 * kTileWaves;
 constexpr int kSingleWaves = 4;   // of the kernel for few rows: each its own keys
 constexpr int kSingleRows = 16;
-constexpr int kSingleKeys = 32;   // keys of a wavefront's step
 constexpr int kMaxRowBytes = KVCACHE_MAX_ATTENTION_HEAD_DIM * 2;
 
 typedef int16_t i16x4 __attribute__((ext_vector_type(4)));
@@ -145,6 +144,20 @@ __device__ __forceinline__ bool clean(u32x4 &p)
     return any;
 }
 
+// Whether there are any in N times eight: without their signs, 16-bit floats
+// order like their bits.
+template <class T, int N>
+__device__ __forceinline__ bool any_special(const u32x4 *p)
+{
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            most = max_halves(most, p[i][j] & 0x7fff7fffu);
+    return (most & 0xffffu) >= T::kExponent || most >> 16 >= T::kExponent;
+}
+
 // Adds the infinities and NaN among four values of a row that is seen.
 template <class H>
 __device__ __forceinline__ void add_special(const uint8_t *at, bool sees, float *o)
@@ -187,18 +200,20 @@ __device__ __forceinline__ Sequence sequence_of(const AttentionArgs &a, uint32_t
 // around each read.)
 static __device__ const u32x4 kZeros[kMaxRowBytes / 16] = {};
 
-// The page of token t < end; ~0 from `end` on, and for a number out of range.
-__device__ __forceinline__ uint32_t page_of(const AttentionArgs &a, const int32_t *table, int32_t t, int32_t end)
+// What the table says for token t, or for the last one from `end` > 0 on.
+// Looked up ahead, and checked (checked_page) where it is used: a check beside
+// the load would wait for it, and for every load before it.
+__device__ __forceinline__ uint32_t raw_page(const AttentionArgs &a, const int32_t *table, int32_t t, int32_t end)
 {
-    uint32_t page = ~0u;
-    if (t < end) {
-        page = (uint32_t)table[a.page_size.div((uint32_t)t)];
-        if (page >= a.num_pages) {
-            set_status(a.status, KVCACHE_BAD_PAGE);
-            page = ~0u;
-        }
-    }
-    return page;
+    return (uint32_t)table[a.page_size.div((uint32_t)(t < end ? t : end - 1))];
+}
+
+// The page of token t < end; ~0 from `end` on, and for a number out of range.
+__device__ __forceinline__ uint32_t checked_page(const AttentionArgs &a, uint32_t raw, int32_t t, int32_t end)
+{
+    if (t < end && raw >= a.num_pages)
+        set_status(a.status, KVCACHE_BAD_PAGE);
+    return t < end && raw < a.num_pages ? raw : ~0u;
 }
 
 // Token t's place in `page`, by an array's strides.
@@ -211,8 +226,15 @@ __device__ __forceinline__ int64_t offset_in(const AttentionArgs &a, uint32_t pa
 __device__ __forceinline__ uint64_t row_address(const AttentionArgs &a, uint32_t page, int32_t t, const uint8_t *base,
                                                 int64_t page_stride, int64_t place_stride, uint32_t esize)
 {
-    return page == ~0u ? (uint64_t)kZeros
-                       : (uint64_t)base + offset_in(a, page, t, page_stride, place_stride) * esize;
+    uint64_t at = (uint64_t)base + offset_in(a, page == ~0u ? 0 : page, t, page_stride, place_stride) * esize;
+    asm volatile("" : "+v"(at));   // picked below, not branched around
+    return page == ~0u ? (uint64_t)kZeros : at;
+}
+
+__device__ __forceinline__ uint64_t scale_address(const AttentionArgs &a, uint32_t page, int32_t t, const float *base,
+                                                  int64_t page_stride, int64_t place_stride)
+{
+    return row_address(a, page, t, (const uint8_t *)base, page_stride, place_stride, 4);
 }
 
 // A piece at an address that came out of shared memory: global, not flat.
@@ -328,19 +350,16 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void kvcache_at
     const bool in = piece * 8 < a.head_dim;
     const uint32_t esize = H::coded ? 1 : 2;
     Piece next[S::kPasses];
-    // of key `lane` of the tile after next, later of the next one
-    uint32_t page = ~0u;
+    // of key `lane` of the tile after next: what the table says
+    uint32_t raw = 0;
     float scale = 0.0f;
 
     auto table_of = [&](uint8_t *buf) { return (uint64_t *)(buf + S::kKBytes + S::kVBytes + S::kScaleBytes); };
     auto scales_of = [&](uint8_t *buf) { return (float *)(buf + S::kKBytes + S::kVBytes); };
-    auto look_up = [&](int32_t t0) {
-        page = ~0u;
-        if (lane < S::kKeys && (H::coded || wave < 2))
-            page = page_of(a, table, t0 + (int32_t)lane, hi);
-    };
+    auto look_up = [&](int32_t t0) { raw = raw_page(a, table, t0 + (int32_t)lane, hi); };
     auto put_table = [&](uint8_t *buf, int32_t t0) {
         const int32_t t = t0 + (int32_t)lane;
+        const uint32_t page = checked_page(a, raw, t, hi);
         if (wave == 0 && lane < S::kKeys)
             table_of(buf)[lane] = row_address(a, page, t, (const uint8_t *)a.k + (int64_t)head * a.k_head * esize,
                                               a.k_page, a.k_place, esize);
@@ -348,12 +367,14 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void kvcache_at
             table_of(buf)[S::kKeys + lane] =
                 row_address(a, page, t, (const uint8_t *)a.v + (int64_t)head * a.v_head * esize, a.v_page, a.v_place, esize);
     };
+    // (raw still of this tile's keys)
     auto load_scales = [&](int32_t t0) {
+        const int32_t t = t0 + (int32_t)lane;
         if (H::coded && wave >= 2) {
-            scale = 0.0f;
-            if (page != ~0u)
-                scale = wave == 2 ? a.k_scale[offset_in(a, page, t0 + (int32_t)lane, a.ks_page, a.ks_place) + head * a.ks_head]
-                                  : a.v_scale[offset_in(a, page, t0 + (int32_t)lane, a.vs_page, a.vs_place) + head * a.vs_head];
+            const uint32_t page = checked_page(a, raw, t, hi);
+            scale = load_at<float>(
+                wave == 2 ? scale_address(a, page, t, a.k_scale + head * a.ks_head, a.ks_page, a.ks_place)
+                          : scale_address(a, page, t, a.v_scale + head * a.vs_head, a.vs_page, a.vs_place));
         }
     };
     auto put_scales = [&](uint8_t *buf) {
@@ -516,7 +537,7 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void kvcache_at
         if (special) {
 #pragma unroll 1
             for (int32_t t = t0; t < t0 + S::kKeys && t < hi; ++t) {
-                const uint32_t from = page_of(a, table, t, hi);
+                const uint32_t from = checked_page(a, raw_page(a, table, t, hi), t, hi);
                 if (from == ~0u)
                     continue;
                 const bool sees = (uint32_t)(t - see_lo) < see_count;
@@ -593,31 +614,43 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void kvcache_at
 //
 // At most 16 rows a (sequence, key/value head), as in a decode step: bound by
 // reading the cache, so everything serves to keep reads in flight.  The keys
-// of a split are dealt to the 4 wavefronts of a workgroup in steps of 32; each
-// keeps its own maximum, sum and output, joined at the end.  A wavefront takes
-// K straight from memory into the matrix instruction's registers, V through
-// registers into shared memory of its own (for the transposing read), and
-// issues the next step's reads as soon as a step's registers are free.
+// of a split are dealt to the 4 wavefronts of a workgroup in steps of kKeys
+// (about 16 KiB of K and V); each keeps its own maximum, sum and output, joined
+// at the end.  A wavefront takes K straight from memory into the matrix
+// instruction's registers, V through registers into shared memory of its own
+// (for the transposing read), and issues the next step's reads as soon as a
+// step's registers are free; their addresses were put into shared memory two
+// steps ahead, one row a lane.
+//
+// The second product has time to spare: where it takes bf16, a weight goes in
+// as its rounding and the rest (two products), so the weights keep 16 bits.  A
+// rest of 0 or of the other sign would turn an infinite value into NaN, so
+// these are taken out here wherever they are.
 
-template <int DP>
+template <class H, int DP>
 struct SingleShape {
+    static constexpr int kKeys = DP == 64 || (DP == 128 && H::coded) ? 64 : 32;
     static constexpr int kVStride = DP * 2 + 32;   // 32 mod 256: see above, for blocks of 16 rows
-    static constexpr int kVBytes = kSingleKeys * kVStride;
-    static constexpr int kWaveBytes = kVBytes + kSingleKeys * (8 + 16);   // and the scales and addresses
+    static constexpr int kVBytes = kKeys * kVStride;
+    static constexpr int kWaveBytes = kVBytes + kKeys * (8 + 16);   // and the scales and addresses
     static constexpr int kPieces = DP / 8;
     static constexpr int kRowsAtOnce = 64 / kPieces;
-    static constexpr int kPasses = kSingleKeys / kRowsAtOnce;
+    static constexpr int kPasses = kKeys / kRowsAtOnce;
+    static constexpr int kBlocks = kKeys / 16;     // of the first product
+    static constexpr int kPairs = kKeys / 32;      // and of the second
     static constexpr int kJoinBytes = kSingleWaves * kSingleRows * (DP + 4) * 4;
     static constexpr int kBytes = kSingleWaves * kWaveBytes > kJoinBytes ? kSingleWaves * kWaveBytes : kJoinBytes;
 };
 
-template <class T, class F, int DP>
-__global__ __launch_bounds__(64 * kSingleWaves) void kvcache_attention_single_kernel(const AttentionArgs a)
+// Full: head_dim is DP, and no piece lies behind a row's end.
+template <class T, class F, int DP, bool Full>
+__global__ __launch_bounds__(64 * kSingleWaves, DP == 256 && __is_same(F, void) ? 1 : 2) void kvcache_attention_single_kernel(const AttentionArgs a)
 {
-    typedef SingleShape<DP> S;
     typedef Held<T, F> H;
+    typedef SingleShape<H, DP> S;
     typedef typename H::V V;
     typedef typename H::piece Piece;
+    constexpr bool kTwice = __is_same(V, Bf16);
     __shared__ __align__(16) uint8_t lds[S::kBytes];
     __shared__ float join_m[kSingleWaves][kSingleRows], join_l[kSingleWaves][kSingleRows];
 
@@ -645,178 +678,220 @@ __global__ __launch_bounds__(64 * kSingleWaves) void kvcache_attention_single_ke
     const int32_t pos = shift + (int32_t)token;
     const int32_t see_hi = held ? (pos < hi - 1 ? pos : hi - 1) : -1;
     const int32_t see_lo = a.window > 0 ? pos - a.window + 1 : 0;
+    // a row sees key t if t - see_lo is below see_count, unsigned
+    const uint32_t see_count = see_hi < see_lo ? 0 : (uint32_t)(see_hi - see_lo) + 1;
 
-    typename T::eight q[DP / 32];
-    {
-        const typename T::elem *at = (const typename T::elem *)a.q + (int64_t)(seq.q0 + token) * a.q_st +
-                                     (int64_t)(head * a.group.d + member) * a.q_sh;
+    uint8_t *vlds = lds + wave * S::kWaveBytes;
+    float *scales = (float *)(vlds + S::kVBytes);                // of the keys, then of the values
+    uint64_t *addresses = (uint64_t *)(scales + 2 * S::kKeys);   // likewise
+    f32x4 o[DP / 16] = {};
+    float m = -__builtin_inff(), l = 0.0f;
+
+    if (lo < hi) {
+        typename T::eight q[DP / 32];
+        const typename T::elem *q_at = (const typename T::elem *)a.q + (int64_t)(seq.q0 + token) * a.q_st +
+                                       (int64_t)(head * a.group.d + member) * a.q_sh;
 #pragma unroll
         for (int s = 0; s < DP / 32; ++s) {
             const uint32_t d = s * 32 + group * 8;
             u32x4 p = {};
-            if (held && d < a.head_dim)
-                p = (*(const u32x4 *)(at + d) & a.q_keep) ^ a.q_flip;
+            if (held && (Full || d < a.head_dim))
+                p = (*(const u32x4 *)(q_at + d) & a.q_keep) ^ a.q_flip;
             q[s] = __builtin_bit_cast(typename T::eight, p);
         }
-    }
 
-    uint8_t *vlds = lds + wave * S::kWaveBytes;
-    float *scales = (float *)(vlds + S::kVBytes);              // 32 of the keys, 32 of the values
-    uint64_t *addresses = (uint64_t *)(scales + 2 * kSingleKeys);   // likewise
-    f32x4 o[DP / 16] = {};
-    float m = -__builtin_inff(), l = 0.0f;
+        const uint32_t esize = H::coded ? 1 : 2;
+        const uint32_t piece = lane % S::kPieces, vkey = lane / S::kPieces;
+        Piece kp[S::kBlocks][DP / 32], vp[S::kPasses];
+        // of key lane % kKeys of a coming step
+        uint32_t raw;
+        uint64_t k_scale_at, v_scale_at;
+        float k_scale = 0.0f, v_scale = 0.0f;
+        const int32_t mine = (int32_t)(lane % S::kKeys);
+        const uint8_t *k_base = (const uint8_t *)a.k + (int64_t)head * a.k_head * esize;
+        const uint8_t *v_base = (const uint8_t *)a.v + (int64_t)head * a.v_head * esize;
 
-    const uint32_t esize = H::coded ? 1 : 2;
-    const uint32_t piece = lane % S::kPieces, vkey = lane / S::kPieces;
-    const bool vin = piece * 8 < a.head_dim;
-    Piece kp[2][DP / 32], vp[S::kPasses];
-    // lanes 0-31: of key `lane` of a coming step; 32-63: of value lane - 32
-    uint32_t page;
-    float scale = 0.0f;
-    const uint8_t *base = lane < 32 ? (const uint8_t *)a.k + (int64_t)head * a.k_head * esize
-                                    : (const uint8_t *)a.v + (int64_t)head * a.v_head * esize;
-    const int64_t page_stride = lane < 32 ? a.k_page : a.v_page, place_stride = lane < 32 ? a.k_place : a.v_place;
-
-    auto look_up = [&](int32_t t0) { page = page_of(a, table, t0 + (int32_t)(lane & 31u), hi); };
-    auto put_table = [&](int32_t t0) {
-        const int32_t t = t0 + (int32_t)(lane & 31u);
-        addresses[lane] = row_address(a, page, t, base, page_stride, place_stride, esize);
-        if (H::coded) {
-            scale = 0.0f;
-            if (page != ~0u)
-                scale = lane < 32 ? a.k_scale[offset_in(a, page, t, a.ks_page, a.ks_place) + head * a.ks_head]
-                                  : a.v_scale[offset_in(a, page, t, a.vs_page, a.vs_place) + head * a.vs_head];
-        }
-    };
-    auto load_rows = [&]() {
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const uint64_t at = addresses[b * 16 + col] + group * 8 * esize;
-#pragma unroll
-            for (int s = 0; s < DP / 32; ++s)
-                kp[b][s] = load_at<Piece>(s * 32 + group * 8 < a.head_dim ? at + s * 32 * esize : (uint64_t)kZeros);
-        }
-#pragma unroll
-        for (int i = 0; i < S::kPasses; ++i) {
-            const uint64_t at = addresses[kSingleKeys + i * S::kRowsAtOnce + vkey] + piece * 8 * esize;
-            vp[i] = load_at<Piece>(vin ? at : (uint64_t)kZeros);
-        }
-    };
-
-    constexpr int kStep = kSingleKeys * kSingleWaves;
-    int32_t t0 = lo + (int32_t)wave * kSingleKeys;
-    look_up(t0);
-    put_table(t0);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    load_rows();
-    float scale_now = scale;
-    look_up(t0 + kStep);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    put_table(t0 + kStep);
-    look_up(t0 + 2 * kStep);
-    for (; t0 < hi; t0 += kStep) {
-        f32x4 s[2] = {};
-#pragma unroll
-        for (int i = 0; i < DP / 32; ++i)
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-                s[b] = T::mfma16(__builtin_bit_cast(typename T::eight, H::key(kp[b][i])), q[i], s[b]);
-        if (H::coded)
-            scales[lane] = scale_now;
-        // not every row sees every key
-        const bool edge = t0 + kSingleKeys - 1 > first || t0 + kSingleKeys > hi ||
-                          (a.window > 0 && t0 <= last - a.window);
-        bool special = false;
-#pragma unroll
-        for (int i = 0; i < S::kPasses; ++i) {
-            u32x4 w = H::value(vp[i]);
-            if (edge)
-                special |= clean<V>(w);
-            *(u32x4 *)(vlds + (i * S::kRowsAtOnce + vkey) * S::kVStride + piece * 16) = w;
-        }
-        // the wavefront's own writes, read back by other lanes of it: in order
-        // in the LDS queue, and kept in order by the compiler
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        scale_now = scale;
-        load_rows();   // of the next step: zeros behind the last key
-
-        // register j of block b is key t0 + 16 b + 4 group + j
-        f32x4 vscale[2];
-        if (H::coded) {
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                s[b] *= *(const f32x4 *)(scales + b * 16 + group * 4);
-                vscale[b] = *(const f32x4 *)(scales + 32 + b * 16 + group * 4);
+        auto look_up = [&](int32_t t0) { raw = raw_page(a, table, t0 + mine, hi); };
+        auto put_table = [&](int32_t t0) {
+            const int32_t t = t0 + mine;
+            const uint32_t page = checked_page(a, raw, t, hi);
+            if (S::kKeys == 64 || lane < 32)
+                addresses[mine] = row_address(a, page, t, k_base, a.k_page, a.k_place, esize);
+            if (S::kKeys == 64 || lane >= 32)
+                addresses[S::kKeys + mine] = row_address(a, page, t, v_base, a.v_page, a.v_place, esize);
+            if (H::coded) {
+                k_scale_at = scale_address(a, page, t, a.k_scale + head * a.ks_head, a.ks_page, a.ks_place);
+                v_scale_at = scale_address(a, page, t, a.v_scale + head * a.vs_head, a.vs_page, a.vs_place);
             }
-        }
-        if (edge) {
+        };
+        auto load_rows = [&]() {
+            if (H::coded) {
+                k_scale = load_at<float>(k_scale_at);
+                v_scale = load_at<float>(v_scale_at);
+            }
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int b = 0; b < S::kBlocks; ++b) {
+                const uint64_t at = addresses[b * 16 + col] + group * 8 * esize;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int32_t t = t0 + b * 16 + (int32_t)group * 4 + j;
-                    s[b][j] = t <= see_hi && t >= see_lo ? s[b][j] : -__builtin_inff();
+                for (int s = 0; s < DP / 32; ++s)
+                    kp[b][s] = load_at<Piece>(Full || s * 32 + group * 8 < a.head_dim ? at + s * 32 * esize
+                                                                                     : (uint64_t)kZeros);
+            }
+#pragma unroll
+            for (int i = 0; i < S::kPasses; ++i) {
+                const uint64_t at = addresses[S::kKeys + i * S::kRowsAtOnce + vkey] + piece * 8 * esize;
+                vp[i] = load_at<Piece>(Full || piece * 8 < a.head_dim ? at : (uint64_t)kZeros);
+            }
+        };
+
+        // A wavefront's own writes to shared memory are read by other lanes of
+        // it: in order in the LDS queue, and kept in order in the code by these
+        // fences, which are no instructions.
+        const auto in_order = [] { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); };
+        constexpr int kStep = S::kKeys * kSingleWaves;
+        int32_t t0 = lo + (int32_t)wave * S::kKeys;
+        look_up(t0);
+        put_table(t0);
+        in_order();
+        load_rows();
+        look_up(t0 + kStep);
+        in_order();
+        put_table(t0 + kStep);
+        look_up(t0 + 2 * kStep);
+        for (; t0 < hi; t0 += kStep) {
+            f32x4 s[S::kBlocks] = {};
+#pragma unroll
+            for (int i = 0; i < DP / 32; ++i)
+#pragma unroll
+                for (int b = 0; b < S::kBlocks; ++b)
+                    s[b] = T::mfma16(__builtin_bit_cast(typename T::eight, H::key(kp[b][i])), q[i], s[b]);
+            if (H::coded) {
+                scales[mine] = k_scale;
+                scales[S::kKeys + mine] = v_scale;
+            }
+            // not every row sees every key
+            const bool edge = t0 + S::kKeys - 1 > first || t0 + S::kKeys > hi ||
+                              (a.window > 0 && t0 <= last - a.window);
+            bool special = false;
+            u32x4 values[S::kPasses];
+#pragma unroll
+            for (int i = 0; i < S::kPasses; ++i)
+                values[i] = H::value(vp[i]);
+            if (!H::coded && kTwice)
+                special = __builtin_amdgcn_ballot_w64(any_special<V, S::kPasses>(values)) != 0;
+            if (special || edge) {
+                special = false;
+#pragma unroll
+                for (int i = 0; i < S::kPasses; ++i)
+                    special |= clean<V>(values[i]);
+                special = __builtin_amdgcn_ballot_w64(special) != 0;
+            }
+#pragma unroll
+            for (int i = 0; i < S::kPasses; ++i)
+                *(u32x4 *)(vlds + (i * S::kRowsAtOnce + vkey) * S::kVStride + piece * 16) = values[i];
+            in_order();
+            load_rows();   // of the next step: zeros behind the last key
+
+            // register j of block b is key t0 + 16 b + 4 group + j
+            if (H::coded) {
+#pragma unroll
+                for (int b = 0; b < S::kBlocks; ++b)
+                    s[b] *= *(const f32x4 *)(scales + b * 16 + group * 4);
+            }
+            if (edge) {
+                const uint32_t see = (uint32_t)(t0 + (int32_t)group * 4 - see_lo);
+#pragma unroll
+                for (int b = 0; b < S::kBlocks; ++b)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        s[b][j] = see + (b * 16 + j) < see_count ? s[b][j] : -__builtin_inff();
+            }
+            float top = s[0][0];
+#pragma unroll
+            for (int b = 0; b < S::kBlocks; ++b)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    top = __builtin_fmaxf(top, s[b][j]);
+            top = __builtin_fmaxf(top, other_half(top));
+            top = __builtin_fmaxf(top, __shfl_xor(top, 16, 64)) * a.scale_log2;
+            if (__builtin_amdgcn_ballot_w64(top > m + kSlack)) {
+                const float grown = __builtin_fmaxf(m, top);
+                const float shrink = m == grown ? 1.0f : __builtin_amdgcn_exp2f(m - grown);
+                m = grown;
+                l *= shrink;
+#pragma unroll
+                for (int d = 0; d < DP / 16; ++d)
+                    o[d] *= shrink;
+            }
+            const float base = m == -__builtin_inff() ? 0.0f : m;
+            typename V::eight p[S::kPairs], rest[S::kPairs];
+#pragma unroll
+            for (int i = 0; i < S::kPairs; ++i) {
+                float w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    w[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * i + j / 4][j % 4], a.scale_log2, -base));
+                    l += w[j];
                 }
-        }
-        float top = s[0][0];
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                top = __builtin_fmaxf(top, s[b][j]);
-        top = __builtin_fmaxf(top, other_half(top));
-        top = __builtin_fmaxf(top, __shfl_xor(top, 16, 64)) * a.scale_log2;
-        if (__builtin_amdgcn_ballot_w64(top > m + kSlack)) {
-            const float grown = __builtin_fmaxf(m, top);
-            const float shrink = m == grown ? 1.0f : __builtin_amdgcn_exp2f(m - grown);
-            m = grown;
-            l *= shrink;
-#pragma unroll
-            for (int d = 0; d < DP / 16; ++d)
-                o[d] *= shrink;
-        }
-        const float base = m == -__builtin_inff() ? 0.0f : m;
-        float w[8];
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                w[4 * b + j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][j], a.scale_log2, -base));
-                l += w[4 * b + j];
                 if (H::coded) {
-                    const float y = w[4 * b + j] * vscale[b][j];
-                    w[4 * b + j] = w[4 * b + j] == 0.0f ? 0.0f : y;
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const f32x4 c = *(const f32x4 *)(scales + S::kKeys + (2 * i + b) * 16 + group * 4);
+                        // a hidden row's scale may be anything
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            w[4 * b + j] = w[4 * b + j] == 0.0f ? 0.0f : w[4 * b + j] * c[j];
+                    }
+                }
+                p[i] = __builtin_bit_cast(typename V::eight, pack8<V>(w));
+                if (kTwice) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float r = w[j] - (float)p[i][j];
+                        w[j] = __builtin_isfinite(w[j]) ? r : 0.0f;
+                    }
+                    rest[i] = __builtin_bit_cast(typename V::eight, pack8<V>(w));
                 }
             }
-        const typename V::eight p = __builtin_bit_cast(typename V::eight, pack8<V>(w));
 
-        // keys 4 group .. + 3 and 16 + 4 group .. + 3, columns 16 d + lane % 16
-        const uint8_t *vat = vlds + (group * 4 + col / 4) * S::kVStride + (col % 4) * 8;
-#pragma unroll
-        for (int d = 0; d < DP / 16; ++d)
-            o[d] = V::mfma16(__builtin_bit_cast(typename V::eight, columns(vat + d * 32, 16 * S::kVStride)), p, o[d]);
-        if (__builtin_amdgcn_ballot_w64(special)) {
+            // keys 4 group .. + 3 and 16 + 4 group .. + 3 of a pair of blocks,
+            // columns 16 d + lane % 16
+            const uint8_t *vat = vlds + (group * 4 + col / 4) * S::kVStride + (col % 4) * 8;
+            const auto read_v = [&](int n) {
+                return __builtin_bit_cast(typename V::eight, columns(vat + n / (DP / 16) * 32 * S::kVStride +
+                                                                     n % (DP / 16) * 32, 16 * S::kVStride));
+            };
+            Feed<typename V::eight, S::kPairs * DP / 16> feed;
+            feed.begin(read_v);
+            feed.run(read_v, [&](int n, typename V::eight v) {
+                const int d = n % (DP / 16), i = n / (DP / 16);
+                o[d] = V::mfma16(v, p[i], o[d]);
+                if (kTwice)
+                    o[d] = V::mfma16(v, rest[i], o[d]);
+            });
+            if (special) {
 #pragma unroll 1
-            for (int32_t t = t0; t < t0 + kSingleKeys && t < hi; ++t) {
-                const uint32_t from = page_of(a, table, t, hi);
-                if (from == ~0u)
-                    continue;
-                const uint8_t *at_v = (const uint8_t *)a.v + ((int64_t)head * a.v_head + group * 4 +
-                                      offset_in(a, from, t, a.v_page, a.v_place)) * esize;
+                for (int32_t t = t0; t < t0 + S::kKeys && t < hi; ++t) {
+                    const uint32_t from = checked_page(a, raw_page(a, table, t, hi), t, hi);
+                    if (from == ~0u)
+                        continue;
+                    const bool sees = (uint32_t)(t - see_lo) < see_count;
+                    const uint8_t *at_v = v_base + (offset_in(a, from, t, a.v_page, a.v_place) + group * 4) * esize;
 #pragma unroll
-                for (int d = 0; d < DP / 16; ++d) {
-                    float x[4] = {};
-                    if (d * 16 + group * 4 < a.head_dim)
-                        add_special<H>(at_v + d * 16 * esize, t <= see_hi && t >= see_lo, x);
-                    o[d] += f32x4{x[0], x[1], x[2], x[3]};
-                    __builtin_amdgcn_sched_barrier(0);
+                    for (int d = 0; d < DP / 16; ++d) {
+                        float x[4] = {};
+                        if (Full || d * 16 + group * 4 < a.head_dim)
+                            add_special<H>(at_v + d * 16 * esize, sees, x);
+                        o[d] += f32x4{x[0], x[1], x[2], x[3]};
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
                 }
             }
+            // the next step's writes stay behind these reads
+            in_order();
+            put_table(t0 + 2 * kStep);
+            look_up(t0 + 3 * kStep);
         }
-        // the next step's writes stay behind these reads
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        put_table(t0 + 2 * kStep);
-        look_up(t0 + 3 * kStep);
     }
 
     // join the four wavefronts
@@ -827,7 +902,7 @@ __global__ __launch_bounds__(64 * kSingleWaves) void kvcache_attention_single_ke
         join_l[wave][col] = l;
     }
     __syncthreads();   // also: every wavefront is done with its V
-    float top = -__builtin_inff(), sum = 0.0f;
+    float top = -__builtin_inff();
 #pragma unroll
     for (int w = 0; w < kSingleWaves; ++w)
         top = __builtin_fmaxf(top, join_m[w][col]);
@@ -843,37 +918,36 @@ __global__ __launch_bounds__(64 * kSingleWaves) void kvcache_attention_single_ke
     // a thread takes 4 columns of a row
     for (uint32_t i = tid; i < rows * (DP / 4); i += 64 * kSingleWaves) {
         const uint32_t r = i / (DP / 4), d = i % (DP / 4) * 4;
-        if (d >= a.head_dim)
+        if (!Full && d >= a.head_dim)
             continue;
         f32x4 y = {};
+        float row_top = -__builtin_inff(), sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kSingleWaves; ++w)
+        for (int w = 0; w < kSingleWaves; ++w) {
             y += *(const f32x4 *)(joined + (w * kSingleRows + r) * (DP + 4) + d);
-        float rtop = -__builtin_inff();
+            row_top = __builtin_fmaxf(row_top, join_m[w][r]);
+        }
 #pragma unroll
         for (int w = 0; w < kSingleWaves; ++w)
-            rtop = __builtin_fmaxf(rtop, join_m[w][r]);
-        sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kSingleWaves; ++w)
-            sum += join_m[w][r] == rtop ? join_l[w][r]
-                                        : join_l[w][r] * __builtin_amdgcn_exp2f(join_m[w][r] - rtop);
+            sum += join_m[w][r] == row_top ? join_l[w][r]
+                                           : join_l[w][r] * __builtin_amdgcn_exp2f(join_m[w][r] - row_top);
         const uint32_t tok = a.group.div(r), qhead = head * a.group.d + a.group.mod(r, tok);
         const int64_t qtoken = seq.q0 + tok;
         if (a.splits > 1) {
             const int64_t part = ((int64_t)split * a.total_q + qtoken) * a.q_heads + qhead;
             if (d == 0) {
-                a.part_ml[2 * part] = rtop;
+                a.part_ml[2 * part] = row_top;
                 a.part_ml[2 * part + 1] = sum;
             }
-            *(f32x4 *)(a.part_o + part * a.head_dim + d) = y;
+            if (sum != 0.0f)   // else not read
+                *(f32x4 *)(a.part_o + part * a.head_dim + d) = y;
         } else {
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
             const float z[4] = {y.x * inv, y.y * inv, y.z * inv, y.w * inv};
             store4<T>((typename T::elem *)a.out + qtoken * a.o_st + qhead * a.o_sh + d, z);
             if (a.lse && d == 0)
                 a.lse[qtoken * a.l_st + qhead * a.l_sh] =
-                    sum == 0.0f ? -__builtin_inff() : (rtop + __builtin_log2f(sum)) * kLn2;
+                    sum == 0.0f ? -__builtin_inff() : (row_top + __builtin_log2f(sum)) * kLn2;
         }
     }
 }
@@ -921,8 +995,11 @@ __global__ __launch_bounds__(256) void kvcache_attention_join_kernel(const Atten
 template <class T, class F, int DP>
 void attention_pick(const AttentionArgs &a, const AttentionShape &shape, uint32_t num_seqs, hipStream_t s)
 {
-    if (shape.single)
-        hipLaunchKernelGGL((kvcache_attention_single_kernel<T, F, DP>), dim3(a.kv_heads * a.splits, num_seqs),
+    if (shape.single && a.head_dim == DP)
+        hipLaunchKernelGGL((kvcache_attention_single_kernel<T, F, DP, true>), dim3(a.kv_heads * a.splits, num_seqs),
+                           dim3(64 * kSingleWaves), 0, s, a);
+    else if (shape.single)
+        hipLaunchKernelGGL((kvcache_attention_single_kernel<T, F, DP, false>), dim3(a.kv_heads * a.splits, num_seqs),
                            dim3(64 * kSingleWaves), 0, s, a);
     else
         hipLaunchKernelGGL((kvcache_attention_tile_kernel<T, F, DP>),
@@ -971,15 +1048,15 @@ AttentionShape attention_shape(uint32_t num_seqs, uint32_t total_q, uint32_t q_h
     const uint64_t rows = (uint64_t)max_q_len * (q_heads / kv_heads);
     r.single = rows <= (uint64_t)kSingleRows;
     r.tiles = r.single ? 1 : (uint32_t)((rows + kTileRows - 1) / kTileRows);
-    const uint64_t fill = r.single ? 768 : 512;
+    const uint64_t fill = r.single ? 2048 : 512;
     const uint64_t blocks = (uint64_t)num_seqs * kv_heads * r.tiles;
-    const uint32_t least = r.single ? 256 : 512;
+    const uint32_t least = 512;
     (void)window;
     uint64_t splits = blocks ? fill / blocks : 1;
     const uint64_t most = (max_context + least - 1) / least;
     splits = splits < most ? splits : most;
     splits = splits ? splits : 1;
-    const uint32_t unit = 128;
+    const uint32_t unit = r.single ? 256 : 128;
     uint64_t keys = ((uint64_t)max_context + splits - 1) / splits;
     keys = (keys + unit - 1) / unit * unit;
     keys = keys ? keys : unit;

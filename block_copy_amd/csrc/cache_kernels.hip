@@ -156,15 +156,6 @@ struct Quantiser {
     }
 };
 
-// The larger of each half of two words, as unsigned 16-bit numbers: without
-// their signs, 16-bit floats order like their bits (NaN above infinity).
-__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
-{
-    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
-                                                                  __builtin_bit_cast(u16x2, b)));
-}
-
 template <class T>
 __device__ __forceinline__ float value_of(uint32_t bits)
 {
@@ -203,11 +194,11 @@ __global__ __launch_bounds__(kThreads) void kvcache_write_kernel(const RowArgs a
                 if (in && slot >= 0)
                     *(u32x4 *)((typename T::elem *)a.pages[i] + at) = p[i];
             } else {
-                uint32_t m = max2(max2(p[i].x & 0x7fff7fffu, p[i].y & 0x7fff7fffu),
-                                  max2(p[i].z & 0x7fff7fffu, p[i].w & 0x7fff7fffu));
+                uint32_t m = max_halves(max_halves(p[i].x & 0x7fff7fffu, p[i].y & 0x7fff7fffu),
+                                  max_halves(p[i].z & 0x7fff7fffu, p[i].w & 0x7fff7fffu));
 #pragma unroll
                 for (int x = 1; x < Lanes; x <<= 1)
-                    m = max2(m, __shfl_xor(m, x, 64));
+                    m = max_halves(m, __shfl_xor(m, x, 64));
                 m = (m >> 16) > (m & 0xffffu) ? m >> 16 : m & 0xffffu;
                 const Quantiser quant(value_of<T>(m < T::kExponent ? m : 0), Format::kQ,
                                       m < T::kExponent);

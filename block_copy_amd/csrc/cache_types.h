@@ -182,6 +182,15 @@ struct Widen<Fp16, Fp8> {
     }
 };
 
+// The larger of each half of two words, as unsigned 16-bit numbers: without
+// their signs, 16-bit floats order like their bits (NaN above infinity).
+__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b)
+{
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
+                                                                  __builtin_bit_cast(u16x2, b)));
+}
+
 __device__ __forceinline__ void set_status(uint32_t *status, uint32_t bit)
 {
     if (status)

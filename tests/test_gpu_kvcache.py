@@ -354,6 +354,24 @@ def test_unseen_values_never_matter(C, kind, q_lens, ctx, heads):
         assert got[..., 34:].isfinite().all()
 
 
+@pytest.mark.parametrize("kind", [BF, FP])
+@pytest.mark.parametrize("q_len", [1, 40])
+def test_seen_infinities(C, q_len, kind):
+    """Infinities and NaN among values that every row sees, far from any edge."""
+    def spoil(kp, vp, table, ks, vs):
+        at = int(table[0][1])
+        vp[at, :, 3, 5], vp[at, :, 4, 6], vp[at, :, 5, 7] = math.inf, -math.inf, math.nan
+        vp[at, :, 6, 8], vp[at, :, 7, 8] = math.inf, -math.inf
+    c = _case(q_lens=[q_len], ctx=[400], heads=4, kv=1, dim=64, page=16, dtype=kind, kind=kind)
+    a = _attend(C, torch.Generator().manual_seed(5), **c)
+    b = _attend(C, torch.Generator().manual_seed(5), edit=spoil, **c)
+    keep = torch.ones(64, dtype=torch.bool)
+    keep[5:9] = False
+    assert _eq_bits(a["out"][..., keep], b["out"][..., keep])
+    o = b["out"].float()
+    assert (o[..., 5] == math.inf).all() and (o[..., 6] == -math.inf).all() and o[..., 7:9].isnan().all()
+
+
 @pytest.mark.parametrize("q_len", [1, 40])
 def test_extreme_scores(C, q_len):
     """Large scores of both signs: the running maximum grows and shrinks."""
