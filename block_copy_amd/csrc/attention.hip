@@ -954,42 +954,76 @@ __global__ __launch_bounds__(64 * kSingleWaves, DP == 256 && __is_same(F, void) 
 
 // ---- joining splits ---------------------------------------------------------
 //
-// A wavefront to a row: out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s,
-// in the order of the splits.  A split without keys has l = 0 and is not read.
+// out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s.  A workgroup to a row:
+// its threads take 4 columns of a split each, as many splits at once as fit,
+// so the reads do not wait for each other (a wavefront that walked the splits
+// took 13 us over 20 of them); sums are in a fixed order.  A split without
+// keys has l = 0 and is not read.
+
+constexpr int kJoinThreads = 256;
+constexpr uint32_t kMaxSplits = kJoinThreads;
 
 template <class T>
-__global__ __launch_bounds__(256) void kvcache_attention_join_kernel(const AttentionArgs a)
+__global__ __launch_bounds__(kJoinThreads) void kvcache_attention_join_kernel(const AttentionArgs a)
 {
-    const uint32_t lane = threadIdx.x & 63u;
-    const int64_t rows = (int64_t)a.total_q * a.q_heads;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (row >= rows)
-        return;
-    float m = -__builtin_inff();
-    for (uint32_t s = 0; s < a.splits; ++s) {
-        if (a.part_ml[2 * (s * rows + row) + 1] != 0.0f)
-            m = __builtin_fmaxf(m, a.part_ml[2 * (s * rows + row)]);
+    __shared__ float weight[kMaxSplits];
+    __shared__ float wave_m[kJoinThreads / 64], wave_l[kJoinThreads / 64];
+    __shared__ __align__(16) f32x4 part[kJoinThreads];
+    const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
+    const int64_t rows = (int64_t)a.total_q * a.q_heads, row = blockIdx.x;
+
+    float m = -__builtin_inff(), l = 0.0f;
+    if (tid < a.splits) {
+        const f32x2 ml = *(const f32x2 *)(a.part_ml + 2 * (tid * rows + row));
+        l = ml.y;
+        m = l == 0.0f ? m : ml.x;
     }
-    float l = 0.0f;
+    float top = m;
+    for (int x = 1; x < 64; x <<= 1)
+        top = __builtin_fmaxf(top, __shfl_xor(top, x, 64));
+    if (lane == 0)
+        wave_m[wave] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 64; ++w)
+        top = __builtin_fmaxf(top, wave_m[w]);
+    const float f = l == 0.0f ? 0.0f : m == top ? 1.0f : __builtin_amdgcn_exp2f(m - top);
+    weight[tid] = f;
+    l = l == 0.0f ? 0.0f : l * f;
+    for (int x = 1; x < 64; x <<= 1)
+        l += __shfl_xor(l, x, 64);
+    if (lane == 0)
+        wave_l[wave] = l;
+    __syncthreads();
+    l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 64; ++w)
+        l += wave_l[w];
+
+    const uint32_t quads = a.head_dim / 4, at_once = kJoinThreads / quads;   // head_dim <= 256: 4 at least
+    const uint32_t quad = tid % quads, first = tid / quads;
     f32x4 y = {};
-    const uint32_t d = lane * 4;
-    for (uint32_t s = 0; s < a.splits; ++s) {
-        const float ms = a.part_ml[2 * (s * rows + row)], ls = a.part_ml[2 * (s * rows + row) + 1];
-        if (ls == 0.0f)
-            continue;
-        const float f = ms == m ? 1.0f : __builtin_amdgcn_exp2f(ms - m);
-        l += ls * f;
-        if (d < a.head_dim)
-            y += *(const f32x4 *)(a.part_o + (s * rows + row) * a.head_dim + d) * f;
+    if (first < at_once) {
+#pragma unroll 4
+        for (uint32_t s = first; s < a.splits; s += at_once) {
+            // a weight of 0 is a split that may not have been written
+            const float w = weight[s];
+            if (w != 0.0f)
+                y += *(const f32x4 *)(a.part_o + (s * rows + row) * a.head_dim + quad * 4) * w;
+        }
     }
+    part[tid] = y;
+    __syncthreads();
+    if (first != 0)
+        return;
+    for (uint32_t i = 1; i < at_once; ++i)
+        y += part[i * quads + quad];
     const int64_t token = row / a.q_heads, head = row % a.q_heads;
-    if (a.lse && lane == 0)
-        a.lse[token * a.l_st + head * a.l_sh] = l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l)) * kLn2;
-    if (d < a.head_dim) {
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        const float z[4] = {y.x * inv, y.y * inv, y.z * inv, y.w * inv};
-        store4<T>((typename T::elem *)a.out + token * a.o_st + head * a.o_sh + d, z);
-    }
+    if (a.lse && quad == 0)
+        a.lse[token * a.l_st + head * a.l_sh] = l == 0.0f ? -__builtin_inff() : (top + __builtin_log2f(l)) * kLn2;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const float z[4] = {y.x * inv, y.y * inv, y.z * inv, y.w * inv};
+    store4<T>((typename T::elem *)a.out + token * a.o_st + head * a.o_sh + quad * 4, z);
 }
 
 template <class T, class F, int DP>
@@ -1031,7 +1065,7 @@ hipError_t attention_type(const AttentionArgs &a, const AttentionShape &shape, u
     if (e != hipSuccess || a.splits == 1)
         return e;
     const uint64_t rows = (uint64_t)a.total_q * a.q_heads;
-    hipLaunchKernelGGL((kvcache_attention_join_kernel<T>), dim3((uint32_t)((rows + 3) / 4)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((kvcache_attention_join_kernel<T>), dim3((uint32_t)rows), dim3(kJoinThreads), 0, s, a);
     return hipGetLastError();
 }
 
@@ -1055,6 +1089,7 @@ AttentionShape attention_shape(uint32_t num_seqs, uint32_t total_q, uint32_t q_h
     uint64_t splits = blocks ? fill / blocks : 1;
     const uint64_t most = (max_context + least - 1) / least;
     splits = splits < most ? splits : most;
+    splits = splits < kMaxSplits ? splits : kMaxSplits;
     splits = splits ? splits : 1;
     const uint32_t unit = r.single ? 256 : 128;
     uint64_t keys = ((uint64_t)max_context + splits - 1) / splits;

@@ -27,6 +27,7 @@ SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
 EXPORTS = ("kvcache_rope_frequencies", "kvcache_rope", "kvcache_write", "kvcache_read",
            "kvcache_attention_workspace_bytes", "kvcache_attention")
 
+_ROW_TYPES = (torch.bfloat16, torch.float16, torch.float32)
 _TYPES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32,
           torch.float8_e4m3fn: FP8, torch.int8: INT8}
 
@@ -106,40 +107,46 @@ def _require(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream   # a tenth of the cost of torch.cuda.current_stream
+
+
 def _call(fn, where: str, device, stream, *args) -> None:
     """fn(*args, stream) with `device` current."""
     index = device.index
     if stream is None:
-        handle = torch.cuda.current_stream(device).cuda_stream
+        handle = _raw_stream(index)
     else:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     if torch.cuda.current_device() == index:
-        _check(fn(*args, handle), where)
+        rc = fn(*args, handle)
     else:
         with torch.cuda.device(index):
-            _check(fn(*args, handle), where)
+            rc = fn(*args, handle)
+    if rc != OK:
+        raise KvcopyError(rc, where)
 
+
+# These run on every call: messages are made only when they are raised.
 
 def _status(status, device):
     if status is None:
         return None
-    _require(status.device == device and status.dtype in (torch.int32, torch.uint32)
-             and status.numel() >= 1, "status must be an int32 tensor on the same device")
+    if status.device != device or status.dtype not in (torch.int32, torch.uint32) or status.numel() < 1:
+        raise ValueError("status must be an int32 tensor on the same device")
     return status.data_ptr()
 
 
 def _vector(t, dtype, n, device, what):
-    _require(t.dtype == dtype and t.device == device and t.dim() == 1 and t.shape[0] == n
-             and (n <= 1 or t.stride(0) == 1),
-             f"{what} must be a contiguous {dtype} vector of {n} on {device}")
+    if t.dtype != dtype or t.device != device or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{what} must be a contiguous {dtype} vector of {n} on {device}")
     return t.data_ptr()
 
 
 def _rows(t, shape, dtype, device, what):
-    _require(t.dtype == dtype and t.device == device and tuple(t.shape) == shape,
-             f"{what} must be {dtype} of shape {shape} on {device}")
     st = t.stride()
-    _require(st[2] == 1 or shape[2] == 1, f"{what}: the last dimension must be contiguous")
+    if t.dtype != dtype or t.device != device or t.shape != shape or (st[2] != 1 and shape[2] != 1):
+        raise ValueError(f"{what} must be {dtype} of shape {tuple(shape)} on {device}, "
+                         "its last dimension contiguous")
     return Rows(t.data_ptr(), st[0], st[1])
 
 
@@ -162,27 +169,29 @@ def rope(positions, freqs, q, k=None, *, q_out=None, k_out=None, interleaved: bo
     kvcache_rope): positions int32 [tokens], freqs float64 [rot_dim / 2].
     q_out and k_out default to new tensors and may be q and k themselves.
     Returns (q_out, k_out)."""
-    _require(q.dim() == 3 and q.is_cuda and q.dtype in (torch.bfloat16, torch.float16, torch.float32),
-             "q must be a [tokens, heads, head_dim] bfloat16, float16 or float32 GPU tensor")
-    dev, dt = q.device, q.dtype
-    tokens, heads, dim = q.shape
+    dev, dt, shape = q.device, q.dtype, q.shape
+    if len(shape) != 3 or dev.type != "cuda" or dt not in _ROW_TYPES:
+        raise ValueError("q must be a [tokens, heads, head_dim] bfloat16, float16 or float32 GPU tensor")
+    tokens, heads, dim = shape
+    pairs = freqs.shape[0]
     a = Rope(ctypes.sizeof(Rope), _TYPES[dt],
              (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0), factor)
     a.positions = _vector(positions, torch.int32, tokens, dev, "positions")
-    a.freq = _vector(freqs, torch.float64, freqs.shape[0], dev, "freqs")
-    a.tokens, a.head_dim, a.rot_dim, a.q_heads = tokens, dim, 2 * freqs.shape[0], heads
+    a.freq = _vector(freqs, torch.float64, pairs, dev, "freqs")
+    a.tokens, a.head_dim, a.rot_dim, a.q_heads = tokens, dim, 2 * pairs, heads
     if q_out is None:
-        q_out = torch.empty((tokens, heads, dim), dtype=dt, device=dev)
-    a.q, a.q_out = _rows(q, (tokens, heads, dim), dt, dev, "q"), _rows(q_out, (tokens, heads, dim), dt, dev, "q_out")
+        q_out = torch.empty(shape, dtype=dt, device=dev)
+    a.q, a.q_out = _rows(q, shape, dt, dev, "q"), _rows(q_out, shape, dt, dev, "q_out")
     if k is not None:
-        _require(k.dim() == 3, "k must be [tokens, heads, head_dim]")
-        shape = (tokens, k.shape[1], dim)
+        kshape = k.shape
+        if len(kshape) != 3 or kshape[0] != tokens or kshape[2] != dim:
+            raise ValueError("k must be [tokens, heads, head_dim], with q's tokens and head_dim")
         if k_out is None:
-            k_out = torch.empty(shape, dtype=dt, device=dev)
-        a.k_heads = k.shape[1]
-        a.k, a.k_out = _rows(k, shape, dt, dev, "k"), _rows(k_out, shape, dt, dev, "k_out")
-    else:
-        _require(k_out is None, "k_out without k")
+            k_out = torch.empty(kshape, dtype=dt, device=dev)
+        a.k_heads = kshape[1]
+        a.k, a.k_out = _rows(k, kshape, dt, dev, "k"), _rows(k_out, kshape, dt, dev, "k_out")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
     _call(lib.kvcache_rope, "kvcache_rope", dev, stream, ctypes.byref(a))
     return q_out, k_out
 
@@ -222,7 +231,8 @@ class PagedCache:
 def write(cache: PagedCache, k, v, slots, *, status=None, stream=None) -> None:
     """Writes k and v, [tokens, kv_heads, head_dim], to slots (int64 [tokens];
     negative: left out) of the cache (see kvcache_write)."""
-    _require(k.dim() == 3 and k.dtype in (torch.bfloat16, torch.float16), "k must be a 3-dimensional 16-bit tensor")
+    if k.dim() != 3 or k.dtype not in _ROW_TYPES[:2]:
+        raise ValueError("k must be a 3-dimensional bfloat16 or float16 tensor")
     dev, shape = cache.device, (k.shape[0], cache.kv_heads, cache.head_dim)
     r, w = _rows(k, shape, k.dtype, dev, "k"), _rows(v, shape, k.dtype, dev, "v")
     _call(lib.kvcache_write, "kvcache_write", dev, stream, cache._ref, _TYPES[k.dtype], ctypes.byref(r),
@@ -238,7 +248,8 @@ def read(cache: PagedCache, slots, k_out=None, v_out=None, *, dtype=None, status
     if dtype is None:
         given = k_out if k_out is not None else v_out
         dtype = given.dtype if given is not None else torch.bfloat16 if cache.coded else cache.dtype
-    _require(dtype in (torch.bfloat16, torch.float16, torch.float32), "rows are bfloat16, float16 or float32")
+    if dtype not in _ROW_TYPES:
+        raise ValueError("rows are bfloat16, float16 or float32")
     if k_out is None:
         k_out = torch.empty(shape, dtype=dtype, device=dev)
     if v_out is None:
@@ -286,17 +297,19 @@ class AttentionPlan:
             out = torch.empty(self.shape, dtype=self.dtype, device=dev)
         a.q = _rows(q, self.shape, self.dtype, dev, "q")
         a.out = _rows(out, self.shape, self.dtype, dev, "out")
-        _require(page_table.dtype == torch.int32 and page_table.device == dev and page_table.dim() == 2
-                 and page_table.shape[0] == self.num_seqs and page_table.shape[1] >= self.columns
-                 and (page_table.shape[1] <= 1 or page_table.stride(1) == 1),
-                 f"page_table must be int32 [{self.num_seqs}, >= {self.columns}] with contiguous rows on {dev}")
-        a.page_table, a.table_stride = page_table.data_ptr(), page_table.stride(0)
+        ts, st = page_table.shape, page_table.stride()
+        if (page_table.dtype != torch.int32 or page_table.device != dev or len(ts) != 2 or ts[0] != self.num_seqs
+                or ts[1] < self.columns or (ts[1] > 1 and st[1] != 1)):
+            raise ValueError(f"page_table must be int32 [{self.num_seqs}, >= {self.columns}] with contiguous rows "
+                             f"on {dev}")
+        a.page_table, a.table_stride = page_table.data_ptr(), st[0]
         a.q_starts = _vector(q_starts, torch.int32, self.num_seqs + 1, dev, "q_starts")
         a.context_lens = _vector(context_lens, torch.int32, self.num_seqs, dev, "context_lens")
         if lse is not None:
-            _require(lse.dtype == torch.float32 and lse.device == dev and tuple(lse.shape) == self.shape[:2],
-                     f"lse must be float32 {self.shape[:2]} on {dev}")
-            a.lse, a.lse_token_stride, a.lse_head_stride = lse.data_ptr(), lse.stride(0), lse.stride(1)
+            if lse.dtype != torch.float32 or lse.device != dev or lse.shape != self.shape[:2]:
+                raise ValueError(f"lse must be float32 {self.shape[:2]} on {dev}")
+            a.lse_token_stride, a.lse_head_stride = lse.stride()
+            a.lse = lse.data_ptr()
         else:
             a.lse = None
         a.status = _status(status, dev)
