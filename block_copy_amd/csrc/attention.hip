@@ -35,8 +35,6 @@ namespace {
 
 constexpr float kSlack = 8.0f;
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr int kTileWaves = 4;     // wavefronts of a tile kernel's workgroup, 32 rows each
-constexpr int kTileRows = 32 * kTileWaves;
 constexpr int kSingleWaves = 4;   // of the kernel for few rows: each its own keys
 constexpr int kSingleRows = 16;
 constexpr int kMaxRowBytes = KVCACHE_MAX_ATTENTION_HEAD_DIM * 2;
@@ -256,43 +254,75 @@ __device__ __forceinline__ void store4(typename T::elem *out, const float *x)
 
 // ---- many rows --------------------------------------------------------------
 //
-// A workgroup of 4 wavefronts takes 128 rows of one (sequence, key/value head)
-// and walks the keys in tiles of Keys, all wavefronts reading the same tile
-// from shared memory.  The next tile's rows are in flight to registers while a
-// tile is worked on, and go to the other shared buffer at its end: one barrier
-// a tile.  Their addresses come from a table in shared memory, which two
-// wavefronts fill a tile ahead, one key a lane (the other two fetch an 8-bit
-// format's scales): worked out by every thread for its own pieces they took
-// more vector instructions than the softmax.  Rows of shared memory are padded so that neither the 16-byte reads
-// of K (stride = 16 bytes mod 256) nor the transposing reads of V (64 mod 256)
-// meet in a bank.
+// A workgroup of kWaves wavefronts takes 32 * kWaves rows of one (sequence,
+// key/value head) and walks the keys in tiles of kKeys, all wavefronts reading
+// the same tile from shared memory.  A wavefront's work on tile i is a block of
+// matrix products, O += V(i-1) P(i-1) and S = K(i) Q, and a block of vector
+// arithmetic, the softmax of S; with two wavefronts on a SIMD, one does its
+// products while the other does its softmax: the workgroup's two halves run the
+// same loop, one barrier apart (a "phase" is what lies between two barriers;
+// the first half does products in even phases, the second in odd ones).
+//
+//   phase     first half                           second half
+//   2 i       outputs(i - 1), scores(i)            softmax(i - 1), stage(i)
+//   2 i + 1   softmax(i), stage(i)                 outputs(i - 1), scores(i)
+//
+// stage(i) moves a thread's share of K(i + 1) and V(i) from registers into
+// shared memory and sends for that of K(i + 2) and V(i + 1).  K(i) and V(i - 1)
+// are read in phases 2 i and 2 i + 1 and their successors in the same buffers
+// are written in 2 i + 2 at the earliest, so two buffers do.
+// Addresses of the rows come from a table in shared memory, written by one lane
+// for each key three tiles ahead (worked out by every thread for its own pieces
+// they took more vector instructions than the softmax).
+//
+// Rows of shared memory are padded so that neither the 16-byte reads of K
+// (stride = 16 bytes mod 256) nor the transposing reads of V (64 mod 256) meet
+// in a bank.
 
 template <int DP>
 struct TileShape {
+    // O and Q of head dimension 256 leave no room for a second wavefront on a SIMD
+    static constexpr int kWaves = DP <= 128 ? 8 : 4;
+    static constexpr bool kHalves = kWaves == 8;
+    static constexpr int kRows = 32 * kWaves;
+    static constexpr int kThreads = 64 * kWaves;
     static constexpr int kKeys = DP <= 128 ? 64 : 32;
     static constexpr int kKStride = DP * 2 + 16;
     static constexpr int kVStride = DP * 2 + 64;
     static constexpr int kKBytes = kKeys * kKStride;
     static constexpr int kVBytes = kKeys * kVStride;
-    static constexpr int kScaleBytes = kKeys * 8;
-    static constexpr int kTableBytes = kKeys * 16;                        // addresses of the rows of K and V
-    static constexpr int kBuffer = kKBytes + kVBytes + kScaleBytes + kTableBytes;
     static constexpr int kPieces = DP / 8;                                // of a row
-    static constexpr int kRowsAtOnce = 64 * kTileWaves / kPieces;
+    static constexpr int kRowsAtOnce = kThreads / kPieces;
     static constexpr int kPasses = kKeys / kRowsAtOnce;
+    static constexpr int kRing = 4;                                       // tiles a table or scales are kept for
 };
 
-template <class T, class F, int DP>
-__global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void kvcache_attention_tile_kernel(const AttentionArgs a)
+// All wavefronts' shared memory accesses before it come before those after it.
+__device__ __forceinline__ void local_barrier()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Full: head_dim is DP, and no piece lies behind a row's end.
+template <class T, class F, int DP, bool Full>
+__global__ __launch_bounds__(TileShape<DP>::kThreads, TileShape<DP>::kHalves ? 2 : 1) void
+kvcache_attention_tile_kernel(const AttentionArgs a)
 {
     typedef TileShape<DP> S;
     typedef Held<T, F> H;
     typedef typename H::V V;
     typedef typename H::piece Piece;
-    __shared__ __align__(16) uint8_t lds[2 * S::kBuffer];
+    __shared__ __align__(16) uint8_t k_lds[2][S::kKBytes];
+    __shared__ __align__(16) uint8_t v_lds[2][S::kVBytes];
+    __shared__ uint64_t k_table[S::kRing][S::kKeys], v_table[S::kRing][S::kKeys];
+    __shared__ __align__(16) float k_scales[S::kRing][S::kKeys], v_scales[S::kRing][S::kKeys];
+    __shared__ uint32_t special[2 * S::kRing];   // whether V(i) has infinities or NaN; twice the ring: read late
 
     const uint32_t tid = threadIdx.x, lane = tid & 63u, half = lane >> 5, col = lane & 31u;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const bool second = S::kHalves && wave >= S::kWaves / 2;
     // key/value heads fastest: workgroups next to each other go to different
     // XCDs, so the tiles of one head, which read the same keys, share an L2;
     // the last tiles, with the most keys, come first
@@ -305,10 +335,10 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void kvcache_at
     const int32_t *table = a.table + blockIdx.y * a.table_stride;
 
     const uint32_t rows = (uint32_t)seq.n * a.group.d;
-    const uint32_t row0 = tile * kTileRows;
+    const uint32_t row0 = tile * S::kRows;
     if (row0 >= rows)
         return;
-    const uint32_t row_last = (row0 + kTileRows < rows ? row0 + kTileRows : rows) - 1;
+    const uint32_t row_last = (row0 + S::kRows < rows ? row0 + S::kRows : rows) - 1;
     const int32_t shift = seq.ctx - seq.n;
     const int32_t first = shift + (int32_t)a.group.div(row0), last = shift + (int32_t)a.group.div(row_last);
     const KeyRange seen = key_range(first, last, a.window, seq.bound);
@@ -326,248 +356,289 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void kvcache_at
     const int32_t pos = shift + (int32_t)token;
     const int32_t see_hi = held ? (pos < hi - 1 ? pos : hi - 1) : -1;                 // last key seen
     const int32_t see_lo = a.window > 0 ? pos - a.window + 1 : 0;
-
-    typename T::eight q[DP / 16];
-    {
-        const typename T::elem *at = (const typename T::elem *)a.q + (int64_t)(seq.q0 + token) * a.q_st +
-                                     (int64_t)(head * a.group.d + member) * a.q_sh;
-#pragma unroll
-        for (int s = 0; s < DP / 16; ++s) {
-            const uint32_t d = s * 16 + half * 8;
-            u32x4 p = {};
-            if (held && d < a.head_dim)
-                p = (*(const u32x4 *)(at + d) & a.q_keep) ^ a.q_flip;
-            q[s] = __builtin_bit_cast(typename T::eight, p);
-        }
-    }
+    // a row sees key t if t - see_lo is below see_count, unsigned
+    const uint32_t see_count = see_hi < see_lo ? 0 : (uint32_t)(see_hi - see_lo) + 1;
 
     f32x16 o[DP / 32] = {};
     float m = -__builtin_inff(), l = 0.0f;
 
-    // rows of the next tile on their way: thread tid takes piece tid % kPieces
-    // of key tid / kPieces + i * kRowsAtOnce
-    const uint32_t piece = tid % S::kPieces, key0 = tid / S::kPieces;
-    const bool in = piece * 8 < a.head_dim;
-    const uint32_t esize = H::coded ? 1 : 2;
-    Piece next[S::kPasses];
-    // of key `lane` of the tile after next: what the table says
-    uint32_t raw = 0;
-    float scale = 0.0f;
-
-    auto table_of = [&](uint8_t *buf) { return (uint64_t *)(buf + S::kKBytes + S::kVBytes + S::kScaleBytes); };
-    auto scales_of = [&](uint8_t *buf) { return (float *)(buf + S::kKBytes + S::kVBytes); };
-    auto look_up = [&](int32_t t0) { raw = raw_page(a, table, t0 + (int32_t)lane, hi); };
-    auto put_table = [&](uint8_t *buf, int32_t t0) {
-        const int32_t t = t0 + (int32_t)lane;
-        const uint32_t page = checked_page(a, raw, t, hi);
-        if (wave == 0 && lane < S::kKeys)
-            table_of(buf)[lane] = row_address(a, page, t, (const uint8_t *)a.k + (int64_t)head * a.k_head * esize,
-                                              a.k_page, a.k_place, esize);
-        if (wave == 1 && lane < S::kKeys)
-            table_of(buf)[S::kKeys + lane] =
-                row_address(a, page, t, (const uint8_t *)a.v + (int64_t)head * a.v_head * esize, a.v_page, a.v_place, esize);
-    };
-    // (raw still of this tile's keys)
-    auto load_scales = [&](int32_t t0) {
-        const int32_t t = t0 + (int32_t)lane;
-        if (H::coded && wave >= 2) {
-            const uint32_t page = checked_page(a, raw, t, hi);
-            scale = load_at<float>(
-                wave == 2 ? scale_address(a, page, t, a.k_scale + head * a.ks_head, a.ks_page, a.ks_place)
-                          : scale_address(a, page, t, a.v_scale + head * a.vs_head, a.vs_page, a.vs_place));
-        }
-    };
-    auto put_scales = [&](uint8_t *buf) {
-        if (H::coded && wave >= 2 && lane < S::kKeys)
-            scales_of(buf)[(wave - 2) * S::kKeys + lane] = scale;
-    };
-    auto load = [&](const uint64_t *addresses) {
-#pragma unroll
-        for (int i = 0; i < S::kPasses; ++i) {
-            const uint64_t at = addresses[key0 + i * S::kRowsAtOnce] + piece * 8 * esize;
-            next[i] = load_at<Piece>(in ? at : (uint64_t)kZeros);
-        }
-    };
-    auto put_keys = [&](uint8_t *buf) {
-#pragma unroll
-        for (int i = 0; i < S::kPasses; ++i)
-            *(u32x4 *)(buf + (key0 + i * S::kRowsAtOnce) * S::kKStride + piece * 16) = H::key(next[i]);
-    };
-    // whether infinities or NaN were taken out (on the mask's edge only)
-    auto put_values = [&](uint8_t *buf, bool edge) {
-        bool special = false;
-#pragma unroll
-        for (int i = 0; i < S::kPasses; ++i) {
-            u32x4 w = H::value(next[i]);
-            if (edge)
-                special |= clean<V>(w);
-            *(u32x4 *)(buf + S::kKBytes + (key0 + i * S::kRowsAtOnce) * S::kVStride + piece * 16) = w;
-        }
-        return special;
-    };
-    // not every row sees every key of the tile
-    auto on_edge = [&](int32_t t0) {
-        return t0 + S::kKeys - 1 > first || t0 + S::kKeys > hi || (a.window > 0 && t0 <= last - a.window);
-    };
-    bool edge = on_edge(lo), special = false;
-
-    // the first tile, and the table of the second
     if (lo < hi) {
-        look_up(lo);
-        put_table(lds, lo);
-        load_scales(lo);
-        put_scales(lds);
-        look_up(lo + S::kKeys);
-        put_table(lds + S::kBuffer, lo + S::kKeys);
-        __syncthreads();
-        load(table_of(lds));
-        put_keys(lds);
-        load(table_of(lds) + S::kKeys);
-        special = put_values(lds, edge);
-    }
-    special = __syncthreads_or(special);
-
-    // a row sees key t0 + x if x - see_from is below see_count, unsigned
-    const uint32_t see_count = see_hi < see_lo ? 0 : (uint32_t)(see_hi - see_lo) + 1;
-    uint32_t turn = 0;
-    for (int32_t t0 = lo; t0 < hi; t0 += S::kKeys, turn ^= 1) {
-        uint8_t *buf = lds + turn * S::kBuffer, *other = lds + (turn ^ 1) * S::kBuffer;
-        const bool more = t0 + S::kKeys < hi;
-        if (more) {
-            load(table_of(other));
-            load_scales(t0 + S::kKeys);
-            look_up(t0 + 2 * S::kKeys);
-        }
-        const float *kscale = scales_of(buf), *vscale = kscale + S::kKeys;
-        const uint32_t see = (uint32_t)(t0 + (int32_t)half * 4 - see_lo);
-
-        // scores
-        f32x16 s[S::kKeys / 32];
-        const uint8_t *kat = buf + col * S::kKStride + half * 16;
-        constexpr int kBlocks = S::kKeys / 32;
-        const auto read_k = [&](int n) {
-            return *(const typename T::eight *)(kat + n % kBlocks * 32 * S::kKStride + n / kBlocks * 32);
-        };
-        Feed<typename T::eight, kBlocks * DP / 16> k_feed;
-        k_feed.begin(read_k);
-        k_feed.run(read_k, [&](int n, typename T::eight k) {
-            const int b = n % kBlocks, i = n / kBlocks;
-            s[b] = T::mfma32(k, q[i], i == 0 ? f32x16{} : s[b]);
-        });
-        // values: of a block of 16 keys, keys 4 half .. + 3 and 8 + 4 half .. + 3
-        const uint8_t *vat = buf + S::kKBytes + (half * 4 + (lane % 16) / 4) * S::kVStride +
-                             ((lane / 16) % 2) * 32 + (lane % 4) * 8;
-        const auto read_v = [&](int n) {
-            return __builtin_bit_cast(typename V::eight, columns(vat + n / (DP / 32) * 16 * S::kVStride +
-                                                                 n % (DP / 32) * 64, 8 * S::kVStride));
-        };
-        Feed<typename V::eight, S::kKeys / 16 * DP / 32> v_feed;
-        v_feed.begin(read_v);
-        // register 4 i + j of block b is key t0 + 32 b + 8 i + 4 half + j
-        if (H::coded) {
+        typename T::eight q[DP / 16];
+        {
+            const typename T::elem *at = (const typename T::elem *)a.q + (int64_t)(seq.q0 + token) * a.q_st +
+                                         (int64_t)(head * a.group.d + member) * a.q_sh;
 #pragma unroll
-            for (int b = 0; b < S::kKeys / 32; ++b)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const f32x4 c = *(const f32x4 *)(kscale + b * 32 + i * 8 + half * 4);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        s[b][4 * i + j] *= c[j];
-                }
-        }
-        if (edge) {
-#pragma unroll
-            for (int b = 0; b < S::kKeys / 32; ++b)
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    s[b][i] = see + (b * 32 + (i / 4) * 8 + i % 4) < see_count ? s[b][i] : -__builtin_inff();
-        }
-
-        // the running maximum, in units of log2
-        float top = s[0][0];
-#pragma unroll
-        for (int b = 0; b < S::kKeys / 32; ++b)
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                top = __builtin_fmaxf(top, s[b][i]);
-        top = __builtin_fmaxf(top, other_half(top)) * a.scale_log2;
-        if (__builtin_amdgcn_ballot_w64(top > m + kSlack)) {
-            const float grown = __builtin_fmaxf(m, top);
-            const float shrink = m == grown ? 1.0f : __builtin_amdgcn_exp2f(m - grown);
-            m = grown;
-            l *= shrink;
-#pragma unroll
-            for (int d = 0; d < DP / 32; ++d)
-                o[d] *= shrink;
-        }
-        const float base = m == -__builtin_inff() ? 0.0f : m;
-
-        typename V::eight p[S::kKeys / 16];
-#pragma unroll
-        for (int b = 0; b < S::kKeys / 32; ++b) {
-            float w[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][i], a.scale_log2, -base));
-                l += w[i];
+            for (int s = 0; s < DP / 16; ++s) {
+                const uint32_t d = s * 16 + half * 8;
+                u32x4 p = {};
+                if (held && (Full || d < a.head_dim))
+                    p = (*(const u32x4 *)(at + d) & a.q_keep) ^ a.q_flip;
+                q[s] = __builtin_bit_cast(typename T::eight, p);
             }
+        }
+        const int32_t tiles = (hi - lo + S::kKeys - 1) / S::kKeys;
+        const uint32_t esize = H::coded ? 1 : 2;
+        const uint8_t *k_base = (const uint8_t *)a.k + (int64_t)head * a.k_head * esize;
+        const uint8_t *v_base = (const uint8_t *)a.v + (int64_t)head * a.v_head * esize;
+        const float *ks_base = a.k_scale + (int64_t)head * a.ks_head, *vs_base = a.v_scale + (int64_t)head * a.vs_head;
+
+        // ---- tables and scales: wavefronts 0 and 1 write rows' addresses,
+        // 2 and 3 an 8-bit format's scales, a lane for each key
+        uint32_t raw = 0;       // what the page table says, looked up a tile ahead
+        float scale = 0.0f;
+        const auto look_up = [&](int32_t i) { raw = raw_page(a, table, lo + i * S::kKeys + (int32_t)lane, hi); };
+        const auto write_table = [&](int32_t i) {   // of tile i; raw is its
+            const int32_t t = lo + i * S::kKeys + (int32_t)lane;
+            const uint32_t page = checked_page(a, raw, t, hi);
+            if (wave == 0) {
+                if (lane < S::kKeys)
+                    k_table[i & (S::kRing - 1)][lane] = row_address(a, page, t, k_base, a.k_page, a.k_place, esize);
+                if (lane == 0)
+                    special[i & (2 * S::kRing - 1)] = 0;
+            } else if (lane < S::kKeys) {
+                v_table[i & (S::kRing - 1)][lane] = row_address(a, page, t, v_base, a.v_page, a.v_place, esize);
+            }
+        };
+        const auto load_scale = [&](int32_t i) {
+            const int32_t t = lo + i * S::kKeys + (int32_t)lane;
+            const uint32_t page = checked_page(a, raw, t, hi);
+            scale = load_at<float>(wave == 2 ? scale_address(a, page, t, ks_base, a.ks_page, a.ks_place)
+                                             : scale_address(a, page, t, vs_base, a.vs_page, a.vs_place));
+        };
+        const auto write_scale = [&](int32_t i) {
+            if (lane < S::kKeys)
+                (wave == 2 ? k_scales : v_scales)[i & (S::kRing - 1)][lane] = scale;
+        };
+        // what goes with softmax(i) in these wavefronts
+        const auto ahead = [&](int32_t i) {
+            if (wave < 2) {
+                write_table(i + 3);
+                look_up(i + 4);
+            } else if (H::coded && wave < 4) {
+                write_scale(i + 1);
+                load_scale(i + 2);
+                look_up(i + 3);
+            }
+        };
+
+        // ---- a thread's share of the rows: piece tid % kPieces of keys
+        // tid / kPieces + j * kRowsAtOnce
+        const uint32_t piece = tid % S::kPieces, key0 = tid / S::kPieces;
+        const bool in = Full || piece * 8 < a.head_dim;
+        Piece k_next[S::kPasses], v_next[S::kPasses];
+        const auto load = [&](Piece *next, const uint64_t *addresses) {
+#pragma unroll
+            for (int j = 0; j < S::kPasses; ++j) {
+                const uint64_t at = addresses[key0 + j * S::kRowsAtOnce] + piece * 8 * esize;
+                next[j] = load_at<Piece>(in ? at : (uint64_t)kZeros);
+            }
+        };
+        // not every row sees every key of the tile
+        const auto on_edge = [&](int32_t i) {
+            const int32_t t0 = lo + i * S::kKeys;
+            return t0 + S::kKeys - 1 > first || t0 + S::kKeys > hi || (a.window > 0 && t0 <= last - a.window);
+        };
+        const auto put_keys = [&](int32_t i) {
+#pragma unroll
+            for (int j = 0; j < S::kPasses; ++j)
+                *(u32x4 *)(k_lds[i & 1] + (key0 + j * S::kRowsAtOnce) * S::kKStride + piece * 16) = H::key(k_next[j]);
+        };
+        const auto put_values = [&](int32_t i) {
+            const bool edge = on_edge(i);
+            bool any = false;
+#pragma unroll
+            for (int j = 0; j < S::kPasses; ++j) {
+                u32x4 w = H::value(v_next[j]);
+                if (edge)
+                    any |= clean<V>(w);
+                *(u32x4 *)(v_lds[i & 1] + (key0 + j * S::kRowsAtOnce) * S::kVStride + piece * 16) = w;
+            }
+            if (edge && any)
+                special[i & (2 * S::kRing - 1)] = 1;
+        };
+        // Nothing here is conditional on i: what lies behind the last tile reads
+        // as zeros, and a load that may or may not follow another makes a wait
+        // for either a wait for both.
+        const auto put = [&](int32_t i) {
+            put_keys(i + 1);
+            put_values(i);
+        };
+        const auto send = [&](int32_t i) {
+            load(k_next, k_table[(i + 2) & (S::kRing - 1)]);
+            load(v_next, v_table[(i + 1) & (S::kRing - 1)]);
+        };
+
+        // ---- the first tables, scales and rows
+        if (wave < 4) {
+            look_up(0);
+            if (wave < 2)
+                write_table(0);
+            if (H::coded && wave >= 2) {
+                load_scale(0);
+                write_scale(0);
+            }
+            look_up(1);
+            if (wave < 2)
+                write_table(1);
+            if (H::coded && wave >= 2)
+                load_scale(1);
+            look_up(2);
+            if (wave < 2) {
+                write_table(2);
+                look_up(3);
+            }
+        }
+        local_barrier();
+        load(k_next, k_table[0]);
+        put_keys(0);
+        load(k_next, k_table[1]);
+        load(v_next, v_table[0]);
+        if (second) {
+            put(0);
+            send(0);
+        }
+        local_barrier();
+
+        // ---- the two blocks of work
+        f32x16 s[S::kKeys / 32];
+        typename V::eight p[S::kKeys / 16];
+        constexpr int kBlocks = S::kKeys / 32;
+        const uint32_t k_lane = col * S::kKStride + half * 16;
+        // of a block of 16 keys, keys 4 half .. + 3 and 8 + 4 half .. + 3
+        const uint32_t v_lane = (half * 4 + (lane % 16) / 4) * S::kVStride + ((lane / 16) % 2) * 32 + (lane % 4) * 8;
+
+        const auto scores = [&](int32_t i) {
+            const uint8_t *at = k_lds[i & 1] + k_lane;
+            const auto read_k = [&](int n) {
+                return *(const typename T::eight *)(at + n % kBlocks * 32 * S::kKStride + n / kBlocks * 32);
+            };
+            Feed<typename T::eight, kBlocks * DP / 16> feed;
+            feed.begin(read_k);
+            feed.run(read_k, [&](int n, typename T::eight k) {
+                const int b = n % kBlocks, d = n / kBlocks;
+                s[b] = T::mfma32(k, q[d], d == 0 ? f32x16{} : s[b]);
+            });
+        };
+        const auto outputs = [&](int32_t i) {
+            const uint8_t *at = v_lds[i & 1] + v_lane;
+            const auto read_v = [&](int n) {
+                return __builtin_bit_cast(typename V::eight, columns(at + n / (DP / 32) * 16 * S::kVStride +
+                                                                     n % (DP / 32) * 64, 8 * S::kVStride));
+            };
+            Feed<typename V::eight, S::kKeys / 16 * DP / 32> feed;
+            feed.begin(read_v);
+            feed.run(read_v, [&](int n, typename V::eight v) {
+                o[n % (DP / 32)] = V::mfma32(v, p[n / (DP / 32)], o[n % (DP / 32)]);
+            });
+            if (on_edge(i) && __builtin_amdgcn_readfirstlane(special[i & (2 * S::kRing - 1)])) {
+                const int32_t t0 = lo + i * S::kKeys;
+#pragma unroll 1
+                for (int32_t t = t0; t < t0 + S::kKeys && t < hi; ++t) {
+                    const uint32_t from = checked_page(a, raw_page(a, table, t, hi), t, hi);
+                    if (from == ~0u)
+                        continue;
+                    const bool sees = (uint32_t)(t - see_lo) < see_count;
+                    const uint8_t *at_v = v_base + (offset_in(a, from, t, a.v_page, a.v_place) + half * 4) * esize;
+#pragma unroll
+                    for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            float y[4] = {};
+                            if (Full || d * 32 + j * 8 + half * 4 < a.head_dim)
+                                add_special<H>(at_v + (d * 32 + j * 8) * esize, sees, y);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                o[d][4 * j + e] += y[e];
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                }
+            }
+        };
+        const auto softmax = [&](int32_t i) {
+            // register 4 j + e of block b is key t0 + 32 b + 8 j + 4 half + e
+            const float *ks = k_scales[i & (S::kRing - 1)] + half * 4, *vs = v_scales[i & (S::kRing - 1)] + half * 4;
             if (H::coded) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const f32x4 c = *(const f32x4 *)(vscale + b * 32 + i * 8 + half * 4);
-                    // a hidden row's scale may be anything
+                for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        w[4 * i + j] = w[4 * i + j] == 0.0f ? 0.0f : w[4 * i + j] * c[j];
-                }
-            }
-            p[2 * b] = __builtin_bit_cast(typename V::eight, pack8<V>(w));
-            p[2 * b + 1] = __builtin_bit_cast(typename V::eight, pack8<V>(w + 8));
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        if (more) {
-            put_keys(other);
-            load(table_of(other) + S::kKeys);
-        }
-
-        v_feed.run(read_v, [&](int n, typename V::eight v) {
-            o[n % (DP / 32)] = V::mfma32(v, p[n / (DP / 32)], o[n % (DP / 32)]);
-        });
-        __builtin_amdgcn_sched_barrier(0);
-        if (special) {
-#pragma unroll 1
-            for (int32_t t = t0; t < t0 + S::kKeys && t < hi; ++t) {
-                const uint32_t from = checked_page(a, raw_page(a, table, t, hi), t, hi);
-                if (from == ~0u)
-                    continue;
-                const bool sees = (uint32_t)(t - see_lo) < see_count;
-                const uint8_t *at_v = (const uint8_t *)a.v + ((int64_t)head * a.v_head + half * 4 +
-                                      offset_in(a, from, t, a.v_page, a.v_place)) * esize;
+                    for (int j = 0; j < 4; ++j) {
+                        const f32x4 c = *(const f32x4 *)(ks + b * 32 + j * 8);
 #pragma unroll
-                for (int d = 0; d < DP / 32; ++d)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float x[4] = {};
-                        if (d * 32 + i * 8 + half * 4 < a.head_dim)
-                            add_special<H>(at_v + (d * 32 + i * 8) * esize, sees, x);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            o[d][4 * i + j] += x[j];
-                        __builtin_amdgcn_sched_barrier(0);
+                        for (int e = 0; e < 4; ++e)
+                            s[b][4 * j + e] *= c[e];
                     }
             }
-        }
+            if (on_edge(i)) {
+                const uint32_t see = (uint32_t)(lo + i * S::kKeys + (int32_t)half * 4 - see_lo);
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        s[b][j] = see + (b * 32 + (j / 4) * 8 + j % 4) < see_count ? s[b][j] : -__builtin_inff();
+            }
+            // the running maximum, in units of log2
+            float top = s[0][0];
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    top = __builtin_fmaxf(top, s[b][j]);
+            top = __builtin_fmaxf(top, other_half(top)) * a.scale_log2;
+            if (__builtin_amdgcn_ballot_w64(top > m + kSlack)) {
+                const float grown = __builtin_fmaxf(m, top);
+                const float shrink = m == grown ? 1.0f : __builtin_amdgcn_exp2f(m - grown);
+                m = grown;
+                l *= shrink;
+#pragma unroll
+                for (int d = 0; d < DP / 32; ++d)
+                    o[d] *= shrink;
+            }
+            const float base = m == -__builtin_inff() ? 0.0f : m;
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+                float w[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    w[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][j], a.scale_log2, -base));
+                    l += w[j];
+                }
+                if (H::coded) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const f32x4 c = *(const f32x4 *)(vs + b * 32 + j * 8);
+                        // a hidden row's scale may be anything
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[4 * j + e] = w[4 * j + e] == 0.0f ? 0.0f : w[4 * j + e] * c[e];
+                    }
+                }
+                p[2 * b] = __builtin_bit_cast(typename V::eight, pack8<V>(w));
+                p[2 * b + 1] = __builtin_bit_cast(typename V::eight, pack8<V>(w + 8));
+            }
+        };
 
-        if (more) {
-            edge = on_edge(t0 + S::kKeys);
-            special = put_values(other, edge);
-            put_scales(other);
-            put_table(buf, t0 + 2 * S::kKeys);   // its rows have been read: by the last barrier
+        // No condition around the products: where O may or may not have changed
+        // it is copied.  (The scores behind the last tile are of zeros.)
+        if (second)
+            local_barrier();
+        scores(0);
+        __builtin_amdgcn_sched_barrier(0);
+        local_barrier();
+        for (int32_t i = 0; i < tiles; ++i) {
+            const int32_t staged = second ? i + 1 : i;
+            put(staged);
+            ahead(i);
+            send(staged);
+            softmax(i);
+            __builtin_amdgcn_sched_barrier(0);
+            local_barrier();
+            outputs(i);
+            scores(i + 1);
+            __builtin_amdgcn_sched_barrier(0);
+            local_barrier();
         }
-        if (edge)
-            special = __syncthreads_or(special);
-        else
-            __syncthreads();
+        if (S::kHalves && !second)
+            local_barrier();
     }
 
     l += other_half(l);
@@ -585,10 +656,10 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void kvcache_at
 #pragma unroll
         for (int d = 0; d < DP / 32; ++d)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t at_d = d * 32 + i * 8 + half * 4;
-                if (at_d < a.head_dim)
-                    *(f32x4 *)(to + at_d) = f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t at_d = d * 32 + j * 8 + half * 4;
+                if ((Full || at_d < a.head_dim) && l != 0.0f)   // else not read
+                    *(f32x4 *)(to + at_d) = f32x4{o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]};
             }
         return;
     }
@@ -599,13 +670,13 @@ __global__ __launch_bounds__(64 * kTileWaves, DP <= 128 ? 2 : 1) void kvcache_at
 #pragma unroll
     for (int d = 0; d < DP / 32; ++d)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t at_d = d * 32 + i * 8 + half * 4;
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t at_d = d * 32 + j * 8 + half * 4;
             float y[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                y[j] = o[d][4 * i + j] * inv;
-            if (at_d < a.head_dim)
+            for (int e = 0; e < 4; ++e)
+                y[e] = o[d][4 * j + e] * inv;
+            if (Full || at_d < a.head_dim)
                 store4<T>(to + at_d, y);
         }
 }
@@ -954,14 +1025,50 @@ __global__ __launch_bounds__(64 * kSingleWaves, DP == 256 && __is_same(F, void) 
 
 // ---- joining splits ---------------------------------------------------------
 //
-// out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s.  A workgroup to a row:
-// its threads take 4 columns of a split each, as many splits at once as fit,
-// so the reads do not wait for each other (a wavefront that walked the splits
-// took 13 us over 20 of them); sums are in a fixed order.  A split without
-// keys has l = 0 and is not read.
+// out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s, in a fixed order.  A split
+// without keys has l = 0 and is not read.  Over few splits a thread takes 4
+// columns of a row and walks them; over more, a workgroup takes a row, its
+// threads 4 columns of a split each, as many splits at once as fit, so that the
+// reads do not wait for each other (a wavefront that walked 20 splits took
+// 13 us; a workgroup a row over 2 splits of 65,536 rows 90 us).
 
 constexpr int kJoinThreads = 256;
 constexpr uint32_t kMaxSplits = kJoinThreads;
+constexpr uint32_t kFewSplits = 8;
+
+template <class T>
+__global__ __launch_bounds__(kJoinThreads) void kvcache_attention_join_few_kernel(const AttentionArgs a)
+{
+    const uint32_t quads = a.head_dim / 4;
+    const uint64_t rows = (uint64_t)a.total_q * a.q_heads;
+    const uint64_t row = (uint64_t)blockIdx.x * (kJoinThreads / quads) + threadIdx.x / quads;
+    const uint32_t quad = threadIdx.x % quads;
+    if (row >= rows || threadIdx.x / quads >= kJoinThreads / quads)
+        return;
+    f32x2 ml[kFewSplits];
+    float m = -__builtin_inff();
+#pragma unroll
+    for (uint32_t s = 0; s < kFewSplits; ++s) {
+        ml[s] = s < a.splits ? *(const f32x2 *)(a.part_ml + 2 * (s * rows + row)) : f32x2{0.0f, 0.0f};
+        m = ml[s].y == 0.0f ? m : __builtin_fmaxf(m, ml[s].x);
+    }
+    float l = 0.0f;
+    f32x4 y = {};
+#pragma unroll
+    for (uint32_t s = 0; s < kFewSplits; ++s) {
+        if (ml[s].y != 0.0f) {
+            const float w = ml[s].x == m ? 1.0f : __builtin_amdgcn_exp2f(ml[s].x - m);
+            l += ml[s].y * w;
+            y += *(const f32x4 *)(a.part_o + (s * rows + row) * a.head_dim + quad * 4) * w;
+        }
+    }
+    const int64_t token = row / a.q_heads, head = row % a.q_heads;
+    if (a.lse && quad == 0)
+        a.lse[token * a.l_st + head * a.l_sh] = l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l)) * kLn2;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const float z[4] = {y.x * inv, y.y * inv, y.z * inv, y.w * inv};
+    store4<T>((typename T::elem *)a.out + token * a.o_st + head * a.o_sh + quad * 4, z);
+}
 
 template <class T>
 __global__ __launch_bounds__(kJoinThreads) void kvcache_attention_join_kernel(const AttentionArgs a)
@@ -1035,9 +1142,12 @@ void attention_pick(const AttentionArgs &a, const AttentionShape &shape, uint32_
     else if (shape.single)
         hipLaunchKernelGGL((kvcache_attention_single_kernel<T, F, DP, false>), dim3(a.kv_heads * a.splits, num_seqs),
                            dim3(64 * kSingleWaves), 0, s, a);
+    else if (a.head_dim == DP)
+        hipLaunchKernelGGL((kvcache_attention_tile_kernel<T, F, DP, true>),
+                           dim3(a.kv_heads * a.splits * a.tiles, num_seqs), dim3(TileShape<DP>::kThreads), 0, s, a);
     else
-        hipLaunchKernelGGL((kvcache_attention_tile_kernel<T, F, DP>),
-                           dim3(a.kv_heads * a.splits * a.tiles, num_seqs), dim3(64 * kTileWaves), 0, s, a);
+        hipLaunchKernelGGL((kvcache_attention_tile_kernel<T, F, DP, false>),
+                           dim3(a.kv_heads * a.splits * a.tiles, num_seqs), dim3(TileShape<DP>::kThreads), 0, s, a);
 }
 
 template <class T, class F>
@@ -1065,7 +1175,12 @@ hipError_t attention_type(const AttentionArgs &a, const AttentionShape &shape, u
     if (e != hipSuccess || a.splits == 1)
         return e;
     const uint64_t rows = (uint64_t)a.total_q * a.q_heads;
-    hipLaunchKernelGGL((kvcache_attention_join_kernel<T>), dim3((uint32_t)rows), dim3(kJoinThreads), 0, s, a);
+    const uint32_t at_once = kJoinThreads / (a.head_dim / 4);
+    if (a.splits <= kFewSplits)
+        hipLaunchKernelGGL((kvcache_attention_join_few_kernel<T>), dim3((uint32_t)((rows + at_once - 1) / at_once)),
+                           dim3(kJoinThreads), 0, s, a);
+    else
+        hipLaunchKernelGGL((kvcache_attention_join_kernel<T>), dim3((uint32_t)rows), dim3(kJoinThreads), 0, s, a);
     return hipGetLastError();
 }
 
@@ -1081,8 +1196,9 @@ AttentionShape attention_shape(uint32_t num_seqs, uint32_t total_q, uint32_t q_h
     AttentionShape r = {};
     const uint64_t rows = (uint64_t)max_q_len * (q_heads / kv_heads);
     r.single = rows <= (uint64_t)kSingleRows;
-    r.tiles = r.single ? 1 : (uint32_t)((rows + kTileRows - 1) / kTileRows);
-    const uint64_t fill = r.single ? 2048 : 512;
+    const uint32_t tile_rows = head_dim <= 128 ? TileShape<128>::kRows : TileShape<256>::kRows;
+    r.tiles = r.single ? 1 : (uint32_t)((rows + tile_rows - 1) / tile_rows);
+    const uint64_t fill = r.single ? 2048 : 256;
     const uint64_t blocks = (uint64_t)num_seqs * kv_heads * r.tiles;
     const uint32_t least = 512;
     (void)window;
