@@ -48,6 +48,7 @@ typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
 template <class T, class F>
 struct Held {
     static constexpr bool coded = true;
+    static constexpr int kShift = 3;   // log2 of a piece's bytes
     typedef u32x2 piece;   // 8 codes
     typedef Bf16 V;
     static __device__ __forceinline__ u32x4 key(piece p) { return Widen<T, F>::eight(p); }
@@ -62,6 +63,7 @@ struct Held {
 template <class T>
 struct Held<T, void> {
     static constexpr bool coded = false;
+    static constexpr int kShift = 4;
     typedef u32x4 piece;   // 8 values
     typedef T V;
     static __device__ __forceinline__ u32x4 key(piece p) { return p; }
@@ -214,25 +216,17 @@ __device__ __forceinline__ uint32_t checked_page(const AttentionArgs &a, uint32_
     return t < end && raw < a.num_pages ? raw : ~0u;
 }
 
-// Token t's place in `page`, by an array's strides.
-__device__ __forceinline__ int64_t offset_in(const AttentionArgs &a, uint32_t page, int32_t t, int64_t page_stride,
-                                             int64_t place_stride)
+// The address of token t's row: strides in units of 2^Shift bytes, which 32
+// bits hold (a product of 64-bit strides takes three times the instructions).
+template <int Shift>
+__device__ __forceinline__ uint64_t row_address(const AttentionArgs &a, uint32_t page, int32_t t, const void *base,
+                                                uint32_t page_stride, uint32_t place_stride)
 {
-    return page_offset(page, a.page_size.mod((uint32_t)t, a.page_size.div((uint32_t)t)), page_stride, place_stride);
-}
-
-__device__ __forceinline__ uint64_t row_address(const AttentionArgs &a, uint32_t page, int32_t t, const uint8_t *base,
-                                                int64_t page_stride, int64_t place_stride, uint32_t esize)
-{
-    uint64_t at = (uint64_t)base + offset_in(a, page == ~0u ? 0 : page, t, page_stride, place_stride) * esize;
+    const uint32_t place = a.page_size.mod((uint32_t)t, a.page_size.div((uint32_t)t));
+    uint64_t at = (uint64_t)base + (((uint64_t)(page == ~0u ? 0 : page) * page_stride +
+                                     (uint64_t)place * place_stride) << Shift);
     asm volatile("" : "+v"(at));   // picked below, not branched around
     return page == ~0u ? (uint64_t)kZeros : at;
-}
-
-__device__ __forceinline__ uint64_t scale_address(const AttentionArgs &a, uint32_t page, int32_t t, const float *base,
-                                                  int64_t page_stride, int64_t place_stride)
-{
-    return row_address(a, page, t, (const uint8_t *)base, page_stride, place_stride, 4);
 }
 
 // A piece at an address that came out of shared memory: global, not flat.
@@ -264,15 +258,15 @@ __device__ __forceinline__ void store4(typename T::elem *out, const float *x)
 // the first half does products in even phases, the second in odd ones).
 //
 //   phase     first half                           second half
-//   2 i       outputs(i - 1), scores(i)            softmax(i - 1), stage(i)
-//   2 i + 1   softmax(i), stage(i)                 outputs(i - 1), scores(i)
+//   2 i       outputs(i - 1), scores(i)            stage(i), softmax(i - 1)
+//   2 i + 1   stage(i), softmax(i)                 outputs(i - 1), scores(i)
 //
 // stage(i) moves a thread's share of K(i + 1) and V(i) from registers into
 // shared memory and sends for that of K(i + 2) and V(i + 1).  K(i) and V(i - 1)
 // are read in phases 2 i and 2 i + 1 and their successors in the same buffers
 // are written in 2 i + 2 at the earliest, so two buffers do.
 // Addresses of the rows come from a table in shared memory, written by one lane
-// for each key three tiles ahead (worked out by every thread for its own pieces
+// for each key four tiles ahead (worked out by every thread for its own pieces
 // they took more vector instructions than the softmax).
 //
 // Rows of shared memory are padded so that neither the 16-byte reads of K
@@ -342,12 +336,8 @@ kvcache_attention_tile_kernel(const AttentionArgs a)
     const int32_t shift = seq.ctx - seq.n;
     const int32_t first = shift + (int32_t)a.group.div(row0), last = shift + (int32_t)a.group.div(row_last);
     const KeyRange seen = key_range(first, last, a.window, seq.bound);
-    int32_t lo = seen.lo, hi = seen.hi;
-    if (a.splits > 1) {
-        const int32_t from = (int32_t)(split * a.split_keys), to = from + (int32_t)a.split_keys;
-        lo = lo > from ? lo : from;
-        hi = hi < to ? hi : to;
-    }
+    const KeyRange part = split_range(seen, a.window > 0 ? seen.lo : 0, split, a.split_keys);
+    const int32_t lo = part.lo, hi = part.hi;
 
     // this lane's row
     const uint32_t row = row0 + wave * 32 + col;
@@ -392,28 +382,28 @@ kvcache_attention_tile_kernel(const AttentionArgs a)
             const uint32_t page = checked_page(a, raw, t, hi);
             if (wave == 0) {
                 if (lane < S::kKeys)
-                    k_table[i & (S::kRing - 1)][lane] = row_address(a, page, t, k_base, a.k_page, a.k_place, esize);
+                    k_table[i & (S::kRing - 1)][lane] = row_address<H::kShift>(a, page, t, k_base, a.k_page, a.k_place);
                 if (lane == 0)
                     special[i & (2 * S::kRing - 1)] = 0;
             } else if (lane < S::kKeys) {
-                v_table[i & (S::kRing - 1)][lane] = row_address(a, page, t, v_base, a.v_page, a.v_place, esize);
+                v_table[i & (S::kRing - 1)][lane] = row_address<H::kShift>(a, page, t, v_base, a.v_page, a.v_place);
             }
         };
         const auto load_scale = [&](int32_t i) {
             const int32_t t = lo + i * S::kKeys + (int32_t)lane;
             const uint32_t page = checked_page(a, raw, t, hi);
-            scale = load_at<float>(wave == 2 ? scale_address(a, page, t, ks_base, a.ks_page, a.ks_place)
-                                             : scale_address(a, page, t, vs_base, a.vs_page, a.vs_place));
+            scale = load_at<float>(wave == 2 ? row_address<2>(a, page, t, ks_base, a.ks_page, a.ks_place)
+                                             : row_address<2>(a, page, t, vs_base, a.vs_page, a.vs_place));
         };
         const auto write_scale = [&](int32_t i) {
             if (lane < S::kKeys)
                 (wave == 2 ? k_scales : v_scales)[i & (S::kRing - 1)][lane] = scale;
         };
-        // what goes with softmax(i) in these wavefronts
+        // what goes with outputs(i) in these wavefronts
         const auto ahead = [&](int32_t i) {
             if (wave < 2) {
-                write_table(i + 3);
-                look_up(i + 4);
+                write_table(i + 4);
+                look_up(i + 5);
             } else if (H::coded && wave < 4) {
                 write_scale(i + 1);
                 load_scale(i + 2);
@@ -426,12 +416,18 @@ kvcache_attention_tile_kernel(const AttentionArgs a)
         const uint32_t piece = tid % S::kPieces, key0 = tid / S::kPieces;
         const bool in = Full || piece * 8 < a.head_dim;
         Piece k_next[S::kPasses], v_next[S::kPasses];
-        const auto load = [&](Piece *next, const uint64_t *addresses) {
+        uint64_t k_from[S::kPasses], v_from[S::kPasses];   // of the rows sent for next
+        const auto find = [&](int32_t i) {
 #pragma unroll
             for (int j = 0; j < S::kPasses; ++j) {
-                const uint64_t at = addresses[key0 + j * S::kRowsAtOnce] + piece * 8 * esize;
-                next[j] = load_at<Piece>(in ? at : (uint64_t)kZeros);
+                k_from[j] = k_table[(i + 2) & (S::kRing - 1)][key0 + j * S::kRowsAtOnce];
+                v_from[j] = v_table[(i + 1) & (S::kRing - 1)][key0 + j * S::kRowsAtOnce];
             }
+        };
+        const auto load = [&](Piece *next, const uint64_t *from) {
+#pragma unroll
+            for (int j = 0; j < S::kPasses; ++j)
+                next[j] = load_at<Piece>(in ? from[j] + piece * 8 * esize : (uint64_t)kZeros);
         };
         // not every row sees every key of the tile
         const auto on_edge = [&](int32_t i) {
@@ -463,40 +459,39 @@ kvcache_attention_tile_kernel(const AttentionArgs a)
             put_keys(i + 1);
             put_values(i);
         };
-        const auto send = [&](int32_t i) {
-            load(k_next, k_table[(i + 2) & (S::kRing - 1)]);
-            load(v_next, v_table[(i + 1) & (S::kRing - 1)]);
+        const auto send = [&] {
+            load(k_next, k_from);
+            load(v_next, v_from);
         };
 
         // ---- the first tables, scales and rows
-        if (wave < 4) {
+        if (wave < 2) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                look_up(i);
+                write_table(i);
+            }
+            look_up(4);
+        } else if (H::coded && wave < 4) {
             look_up(0);
-            if (wave < 2)
-                write_table(0);
-            if (H::coded && wave >= 2) {
-                load_scale(0);
-                write_scale(0);
-            }
+            load_scale(0);
+            write_scale(0);
             look_up(1);
-            if (wave < 2)
-                write_table(1);
-            if (H::coded && wave >= 2)
-                load_scale(1);
+            load_scale(1);
             look_up(2);
-            if (wave < 2) {
-                write_table(2);
-                look_up(3);
-            }
         }
         local_barrier();
-        load(k_next, k_table[0]);
+        find(-2);
+        load(k_next, k_from);
         put_keys(0);
-        load(k_next, k_table[1]);
-        load(v_next, v_table[0]);
+        find(-1);
+        send();
         if (second) {
             put(0);
-            send(0);
+            find(0);
+            send();
         }
+        find(second ? 1 : 0);
         local_barrier();
 
         // ---- the two blocks of work
@@ -507,27 +502,33 @@ kvcache_attention_tile_kernel(const AttentionArgs a)
         // of a block of 16 keys, keys 4 half .. + 3 and 8 + 4 half .. + 3
         const uint32_t v_lane = (half * 4 + (lane % 16) / 4) * S::kVStride + ((lane / 16) % 2) * 32 + (lane % 4) * 8;
 
+        const auto read_k = [&](int32_t i, int n) {
+            return *(const typename T::eight *)(k_lds[i & 1] + k_lane + n % kBlocks * 32 * S::kKStride + n / kBlocks * 32);
+        };
+        const auto read_v = [&](int32_t i, int n) {
+            return __builtin_bit_cast(typename V::eight,
+                                      columns(v_lds[i & 1] + v_lane + n / (DP / 32) * 16 * S::kVStride +
+                                              n % (DP / 32) * 64, 8 * S::kVStride));
+        };
+        Feed<typename T::eight, kBlocks * DP / 16> k_feed;
+        // K's first reads go out ahead of the outputs where registers are left
+        constexpr bool kEarly = DP <= 128 && Full && !H::coded;
         const auto scores = [&](int32_t i) {
-            const uint8_t *at = k_lds[i & 1] + k_lane;
-            const auto read_k = [&](int n) {
-                return *(const typename T::eight *)(at + n % kBlocks * 32 * S::kKStride + n / kBlocks * 32);
-            };
-            Feed<typename T::eight, kBlocks * DP / 16> feed;
-            feed.begin(read_k);
-            feed.run(read_k, [&](int n, typename T::eight k) {
+            if (!kEarly)
+                k_feed.begin([&](int n) { return read_k(i, n); });
+            k_feed.run([&](int n) { return read_k(i, n); }, [&](int n, typename T::eight k) {
                 const int b = n % kBlocks, d = n / kBlocks;
                 s[b] = T::mfma32(k, q[d], d == 0 ? f32x16{} : s[b]);
             });
         };
         const auto outputs = [&](int32_t i) {
-            const uint8_t *at = v_lds[i & 1] + v_lane;
-            const auto read_v = [&](int n) {
-                return __builtin_bit_cast(typename V::eight, columns(at + n / (DP / 32) * 16 * S::kVStride +
-                                                                     n % (DP / 32) * 64, 8 * S::kVStride));
-            };
             Feed<typename V::eight, S::kKeys / 16 * DP / 32> feed;
-            feed.begin(read_v);
-            feed.run(read_v, [&](int n, typename V::eight v) {
+            feed.begin([&](int n) { return read_v(i, n); });
+            if (kEarly)
+                k_feed.begin([&](int n) { return read_k(i + 1, n); });
+            ahead(i);
+            find(second ? i + 2 : i + 1);
+            feed.run([&](int n) { return read_v(i, n); }, [&](int n, typename V::eight v) {
                 o[n % (DP / 32)] = V::mfma32(v, p[n / (DP / 32)], o[n % (DP / 32)]);
             });
             if (on_edge(i) && __builtin_amdgcn_readfirstlane(special[i & (2 * S::kRing - 1)])) {
@@ -538,7 +539,8 @@ kvcache_attention_tile_kernel(const AttentionArgs a)
                     if (from == ~0u)
                         continue;
                     const bool sees = (uint32_t)(t - see_lo) < see_count;
-                    const uint8_t *at_v = v_base + (offset_in(a, from, t, a.v_page, a.v_place) + half * 4) * esize;
+                    const uint8_t *at_v = (const uint8_t *)row_address<H::kShift>(a, from, t, v_base, a.v_page, a.v_place) +
+                                          half * 4 * esize;
 #pragma unroll
                     for (int d = 0; d < DP / 32; ++d)
 #pragma unroll
@@ -621,14 +623,14 @@ kvcache_attention_tile_kernel(const AttentionArgs a)
         // it is copied.  (The scores behind the last tile are of zeros.)
         if (second)
             local_barrier();
+        if (kEarly)
+            k_feed.begin([&](int n) { return read_k(0, n); });
         scores(0);
         __builtin_amdgcn_sched_barrier(0);
         local_barrier();
         for (int32_t i = 0; i < tiles; ++i) {
-            const int32_t staged = second ? i + 1 : i;
-            put(staged);
-            ahead(i);
-            send(staged);
+            put(second ? i + 1 : i);
+            send();
             softmax(i);
             __builtin_amdgcn_sched_barrier(0);
             local_barrier();
@@ -715,7 +717,7 @@ struct SingleShape {
 
 // Full: head_dim is DP, and no piece lies behind a row's end.
 template <class T, class F, int DP, bool Full>
-__global__ __launch_bounds__(64 * kSingleWaves, DP == 256 && __is_same(F, void) ? 1 : 2) void kvcache_attention_single_kernel(const AttentionArgs a)
+__global__ __launch_bounds__(64 * kSingleWaves, DP == 256 && (__is_same(F, void) || !Full) ? 1 : 2) void kvcache_attention_single_kernel(const AttentionArgs a)
 {
     typedef Held<T, F> H;
     typedef SingleShape<H, DP> S;
@@ -728,8 +730,14 @@ __global__ __launch_bounds__(64 * kSingleWaves, DP == 256 && __is_same(F, void) 
     const uint32_t tid = threadIdx.x, lane = tid & 63u, group = lane >> 4, col = lane & 15u;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t head = blockIdx.x % a.kv_heads, split = blockIdx.x / a.kv_heads;
-    const Sequence seq = sequence_of(a, blockIdx.y);
     const int32_t *table = a.table + blockIdx.y * a.table_stride;
+    // Without a window a split starts where it starts: its first lookup need
+    // not wait for the sequence's length (what it gives is checked later).
+    const int32_t mine = (int32_t)(lane % S::kKeys);   // the key of a step whose row this lane looks up
+    uint32_t raw = 0;
+    if (a.window == 0 && a.max_context > 0)
+        raw = raw_page(a, table, (int32_t)(split * a.split_keys + wave * S::kKeys) + mine, (int32_t)a.max_context);
+    const Sequence seq = sequence_of(a, blockIdx.y);
     uint32_t rows = (uint32_t)seq.n * a.group.d;
     rows = rows < kSingleRows ? rows : kSingleRows;   // more: flagged by sequence_of
     if (rows == 0)
@@ -737,12 +745,8 @@ __global__ __launch_bounds__(64 * kSingleWaves, DP == 256 && __is_same(F, void) 
     const int32_t shift = seq.ctx - seq.n;
     const int32_t first = shift, last = shift + (int32_t)a.group.div(rows - 1);
     const KeyRange seen = key_range(first, last, a.window, seq.bound);
-    int32_t lo = seen.lo, hi = seen.hi;
-    {
-        const int32_t from = (int32_t)(split * a.split_keys), to = from + (int32_t)a.split_keys;
-        lo = lo > from ? lo : from;
-        hi = hi < to ? hi : to;
-    }
+    const KeyRange part = split_range(seen, a.window > 0 ? seen.lo : 0, split, a.split_keys);
+    const int32_t lo = part.lo, hi = part.hi;
 
     const bool held = col < rows;
     const uint32_t token = a.group.div(held ? col : 0), member = a.group.mod(held ? col : 0, token);
@@ -774,11 +778,8 @@ __global__ __launch_bounds__(64 * kSingleWaves, DP == 256 && __is_same(F, void) 
         const uint32_t esize = H::coded ? 1 : 2;
         const uint32_t piece = lane % S::kPieces, vkey = lane / S::kPieces;
         Piece kp[S::kBlocks][DP / 32], vp[S::kPasses];
-        // of key lane % kKeys of a coming step
-        uint32_t raw;
         uint64_t k_scale_at, v_scale_at;
         float k_scale = 0.0f, v_scale = 0.0f;
-        const int32_t mine = (int32_t)(lane % S::kKeys);
         const uint8_t *k_base = (const uint8_t *)a.k + (int64_t)head * a.k_head * esize;
         const uint8_t *v_base = (const uint8_t *)a.v + (int64_t)head * a.v_head * esize;
 
@@ -787,12 +788,12 @@ __global__ __launch_bounds__(64 * kSingleWaves, DP == 256 && __is_same(F, void) 
             const int32_t t = t0 + mine;
             const uint32_t page = checked_page(a, raw, t, hi);
             if (S::kKeys == 64 || lane < 32)
-                addresses[mine] = row_address(a, page, t, k_base, a.k_page, a.k_place, esize);
+                addresses[mine] = row_address<H::kShift>(a, page, t, k_base, a.k_page, a.k_place);
             if (S::kKeys == 64 || lane >= 32)
-                addresses[S::kKeys + mine] = row_address(a, page, t, v_base, a.v_page, a.v_place, esize);
+                addresses[S::kKeys + mine] = row_address<H::kShift>(a, page, t, v_base, a.v_page, a.v_place);
             if (H::coded) {
-                k_scale_at = scale_address(a, page, t, a.k_scale + head * a.ks_head, a.ks_page, a.ks_place);
-                v_scale_at = scale_address(a, page, t, a.v_scale + head * a.vs_head, a.vs_page, a.vs_place);
+                k_scale_at = row_address<2>(a, page, t, a.k_scale + (int64_t)head * a.ks_head, a.ks_page, a.ks_place);
+                v_scale_at = row_address<2>(a, page, t, a.v_scale + (int64_t)head * a.vs_head, a.vs_page, a.vs_place);
             }
         };
         auto load_rows = [&]() {
@@ -821,7 +822,8 @@ __global__ __launch_bounds__(64 * kSingleWaves, DP == 256 && __is_same(F, void) 
         const auto in_order = [] { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); };
         constexpr int kStep = S::kKeys * kSingleWaves;
         int32_t t0 = lo + (int32_t)wave * S::kKeys;
-        look_up(t0);
+        if (a.window > 0)
+            look_up(t0);
         put_table(t0);
         in_order();
         load_rows();
@@ -947,7 +949,8 @@ __global__ __launch_bounds__(64 * kSingleWaves, DP == 256 && __is_same(F, void) 
                     if (from == ~0u)
                         continue;
                     const bool sees = (uint32_t)(t - see_lo) < see_count;
-                    const uint8_t *at_v = v_base + (offset_in(a, from, t, a.v_page, a.v_place) + group * 4) * esize;
+                    const uint8_t *at_v = (const uint8_t *)row_address<H::kShift>(a, from, t, v_base, a.v_page, a.v_place) +
+                                          group * 4 * esize;
 #pragma unroll
                     for (int d = 0; d < DP / 16; ++d) {
                         float x[4] = {};
@@ -1186,33 +1189,52 @@ hipError_t attention_type(const AttentionArgs &a, const AttentionShape &shape, u
 
 }  // namespace
 
-// The layout of a call.  Workgroups wanted: `kFill`, about three to each of
-// 256 CUs (two of the tile kernel); where the rows give fewer, the keys are
-// split, into no fewer than kSplitKeys each.
+// The layout of a call, from its sizes alone.  Where the rows give fewer
+// workgroups than the GPU holds, the keys are split.
+//
+// Few rows: the GPU holds 512 workgroups, and ragged sequences want several
+// times that (12 x 40001 e4m3: 512 workgroups 281 us, 1024 177, 2048 153, 4096
+// 155), of at least 512 keys each; a call too small for that takes splits of
+// one step of a workgroup, for the shortest chain of reads.
+// Many rows: one workgroup to a CU (two splits for each CU's workgroup of 2048
+// of 18432 cost 60 us in writing and joining them).  Tiles are counted from all
+// rows, not from the longest sequence's.
 AttentionShape attention_shape(uint32_t num_seqs, uint32_t total_q, uint32_t q_heads, uint32_t kv_heads,
                                uint32_t head_dim, uint32_t max_q_len, uint32_t max_context,
                                uint32_t window)
 {
     AttentionShape r = {};
-    const uint64_t rows = (uint64_t)max_q_len * (q_heads / kv_heads);
+    const uint32_t group = q_heads / kv_heads;
+    const uint64_t rows = (uint64_t)max_q_len * group;
     r.single = rows <= (uint64_t)kSingleRows;
     const uint32_t tile_rows = head_dim <= 128 ? TileShape<128>::kRows : TileShape<256>::kRows;
     r.tiles = r.single ? 1 : (uint32_t)((rows + tile_rows - 1) / tile_rows);
-    const uint64_t fill = r.single ? 2048 : 256;
-    const uint64_t blocks = (uint64_t)num_seqs * kv_heads * r.tiles;
-    const uint32_t least = 512;
-    (void)window;
-    uint64_t splits = blocks ? fill / blocks : 1;
-    const uint64_t most = (max_context + least - 1) / least;
-    splits = splits < most ? splits : most;
+    // the keys that a workgroup's rows see
+    const uint64_t span = r.single ? max_q_len : tile_rows / group + 2;
+    uint64_t range = max_context;
+    if (window > 0 && window + span < range)
+        range = window + span;
+    uint64_t blocks = (uint64_t)num_seqs * r.tiles;
+    const uint64_t by_rows = (uint64_t)total_q * group / tile_rows + num_seqs;
+    blocks = (r.single || blocks < by_rows ? blocks : by_rows) * kv_heads;
+    blocks = blocks ? blocks : 1;
+    uint64_t splits, unit;
+    if (r.single) {
+        unit = 128;
+        splits = 2048 / blocks < range / 512 ? 2048 / blocks : range / 512;
+        const uint64_t quick = 256 / blocks < range / unit ? 256 / blocks : range / unit;
+        splits = splits > quick ? splits : quick;
+    } else {
+        unit = 128;
+        splits = 256 / blocks < range / 512 ? 256 / blocks : range / 512;
+    }
     splits = splits < kMaxSplits ? splits : kMaxSplits;
     splits = splits ? splits : 1;
-    const uint32_t unit = r.single ? 256 : 128;
-    uint64_t keys = ((uint64_t)max_context + splits - 1) / splits;
+    uint64_t keys = (range + splits - 1) / splits;
     keys = (keys + unit - 1) / unit * unit;
     keys = keys ? keys : unit;
     r.split_keys = (uint32_t)keys;
-    r.splits = (uint32_t)((max_context + keys - 1) / keys);
+    r.splits = (uint32_t)((range + keys - 1) / keys);
     r.splits = r.splits ? r.splits : 1;
     if (r.splits > 1)
         r.workspace_bytes = (uint64_t)r.splits * total_q * q_heads * (head_dim + 2) * 4;

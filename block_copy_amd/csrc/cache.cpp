@@ -112,6 +112,12 @@ int attention_sizes(const kvcache_pages_t *p, const kvcache_attention_t *g)
         return KVCOPY_EINVAL;
     if (g->q_heads == 0 || g->q_heads > kMaxHeads || g->q_heads % p->kv_heads != 0)
         return KVCOPY_EINVAL;
+    for (int i = 0; i < 3; i += 2) {
+        const bool coded = element_bytes(p->format) == 1;
+        if ((uint64_t)p->k_stride[i] >= 1ull << 35 || (uint64_t)p->v_stride[i] >= 1ull << 35 ||
+            (coded && ((uint64_t)p->ks_stride[i] >= 1ull << 32 || (uint64_t)p->vs_stride[i] >= 1ull << 32)))
+            return KVCOPY_EINVAL;
+    }
     const uint64_t group = g->q_heads / p->kv_heads, most = (1ull << 31) - (1ull << 16);
     if (g->num_seqs > 65535 || g->total_q * group >= most || g->max_q_len * group >= most ||
         g->max_context >= most || g->window < 0 || !(std::fabs((double)g->scale) <= 1e38))
@@ -295,18 +301,18 @@ extern "C" int kvcache_attention(const kvcache_pages_t *p, const kvcache_attenti
     a.v = p->v;
     a.k_scale = p->k_scale;
     a.v_scale = p->v_scale;
-    a.k_page = p->k_stride[0];
+    a.k_page = (uint32_t)(p->k_stride[0] / 8);
     a.k_head = p->k_stride[1];
-    a.k_place = p->k_stride[2];
-    a.v_page = p->v_stride[0];
+    a.k_place = (uint32_t)(p->k_stride[2] / 8);
+    a.v_page = (uint32_t)(p->v_stride[0] / 8);
     a.v_head = p->v_stride[1];
-    a.v_place = p->v_stride[2];
-    a.ks_page = p->ks_stride[0];
+    a.v_place = (uint32_t)(p->v_stride[2] / 8);
+    a.ks_page = (uint32_t)p->ks_stride[0];
     a.ks_head = p->ks_stride[1];
-    a.ks_place = p->ks_stride[2];
-    a.vs_page = p->vs_stride[0];
+    a.ks_place = (uint32_t)p->ks_stride[2];
+    a.vs_page = (uint32_t)p->vs_stride[0];
     a.vs_head = p->vs_stride[1];
-    a.vs_place = p->vs_stride[2];
+    a.vs_place = (uint32_t)p->vs_stride[2];
     a.table = g->page_table;
     a.table_stride = g->table_stride;
     a.q_starts = g->q_starts;

@@ -45,8 +45,9 @@ struct AttentionArgs {
     int64_t q_st, q_sh, o_st, o_sh, l_st, l_sh;
     const void *k, *v;
     const float *k_scale, *v_scale;
-    int64_t k_page, k_head, k_place, v_page, v_head, v_place;
-    int64_t ks_page, ks_head, ks_place, vs_page, vs_head, vs_place;
+    int64_t k_head, v_head, ks_head, vs_head;               // in elements
+    uint32_t k_page, k_place, v_page, v_place;              // in pieces of 8 elements
+    uint32_t ks_page, ks_place, vs_page, vs_place;          // in elements
     const int32_t *table;
     int64_t table_stride;
     const int32_t *q_starts, *context_lens;

@@ -64,4 +64,13 @@ KVC_HD KeyRange key_range(int32_t first, int32_t last, int32_t window, int32_t b
     return r;
 }
 
+// Split `split` of such a range: keys base + split * keys .. + keys - 1 of it.
+KVC_HD KeyRange split_range(KeyRange r, int32_t base, uint32_t split, uint32_t keys)
+{
+    const int64_t from = base + (int64_t)split * keys, to = from + keys;
+    r.lo = from > r.lo ? (int32_t)(from < r.hi ? from : r.hi) : r.lo;
+    r.hi = to < r.hi ? (int32_t)to : r.hi;
+    return r;
+}
+
 }  // namespace kvc

@@ -181,7 +181,8 @@ int kvcache_read(const kvcache_pages_t *pages, uint32_t dtype, const kvcache_row
  * Query head h reads key/value head h / (q_heads / kv_heads).  A row that sees
  * no key gives out 0 and lse -infinity.  Keys and values a row does not see
  * never reach it, whatever they hold (an infinity or a NaN among them); those
- * past context_len are not read, nor are page numbers past the last one used.
+ * past context_len are not read, and page numbers past the last one used are
+ * ignored.
  * One new token a sequence (a decode step), a few (a drafted continuation) and
  * long chunks go through the same call.
  *
@@ -200,7 +201,8 @@ int kvcache_read(const kvcache_pages_t *pages, uint32_t dtype, const kvcache_row
  * KVCACHE_MAX_ATTENTION_HEAD_DIM; q_heads no multiple of kv_heads or above
  * 2^16; num_seqs above 65535; total_q, max_q_len * group, max_context >= 2^31
  * - 2^16; table_columns too few for max_context; window negative; scale above
- * 1e38 or NaN; workspace too small; launch beyond the grid's limit), KVCOPY_EALIGN
+ * 1e38 or NaN; a page or place stride negative, or 2^35 or more (a scale's:
+ * 2^32); workspace too small; launch beyond the grid's limit), KVCOPY_EALIGN
  * (head_dim, a stride or an address of q, out or pages no multiple of 8
  * elements; workspace no multiple of 16 bytes), KVCOPY_EHIP.
  */

@@ -64,7 +64,29 @@ int main()
                             }
                         if (k.lo < 0 || k.hi > ctx)
                             fail("bounds", k.lo, k.hi);
+                        // splits of it, from its start or from key 0, hold each key once
+                        for (int keys = 1; keys < 6; ++keys)
+                            for (int base = 0; base <= k.lo; base += k.lo ? k.lo : 1) {
+                                int next = k.lo;
+                                for (int s = 0; s < 20; ++s) {
+                                    const kvc::KeyRange p = kvc::split_range(k, base, s, keys);
+                                    if (p.lo >= p.hi)
+                                        continue;
+                                    if (p.lo != next || p.hi > k.hi || p.hi - p.lo > keys)
+                                        fail("split", p.lo, p.hi);
+                                    next = p.hi;
+                                }
+                                if (k.lo < k.hi && next != k.hi)
+                                    fail("splits", next, k.hi);
+                            }
                     }
+    // at the end of 31 bits
+    {
+        const kvc::KeyRange r = {(int)top - 5000, (int)top - 65536 + 60000};
+        const kvc::KeyRange e = kvc::split_range(r, r.lo, 200, 1u << 30);
+        if (e.lo < e.hi)
+            fail("far split", e.lo, e.hi);
+    }
     printf("ok\n");
     return 0;
 }

@@ -207,6 +207,9 @@ def test_attention_refusals(C):
                dict(q_starts=None), dict(context_lens=None), dict(page_table=None)):
         assert call(**kw) == C.EINVAL, kw
     assert call(_pages(C, format=0), dtype=1) == C.EINVAL
+    for kw in (dict(k_stride=(-2048, 1024, 64)), dict(v_stride=(2048, 1024, -64)), dict(k_stride=(1 << 35, 1024, 64)),
+               dict(ks_stride=(1 << 32, 16, 1)), dict(vs_stride=(32, 16, -1))):
+        assert call(_pages(C, **kw)) == C.EINVAL, kw
     # a workspace that is too small, or missing
     long = dict(num_seqs=1, max_context=4096, table_columns=256)
     pg, a = _attention(C, **long)
