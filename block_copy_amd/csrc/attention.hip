@@ -308,6 +308,9 @@ kvcache_attention_tile_kernel(const AttentionArgs a)
     typedef Held<T, F> H;
     typedef typename H::V V;
     typedef typename H::piece Piece;
+    // fp16 results of 8-bit pages, whose second product takes bf16: each weight
+    // as its rounding and the rest, or the results would keep 8 bits, not 11
+    constexpr bool kTwice = H::coded && __is_same(T, Fp16);
     __shared__ __align__(16) uint8_t k_lds[2][S::kKBytes];
     __shared__ __align__(16) uint8_t v_lds[2][S::kVBytes];
     __shared__ uint64_t k_table[S::kRing][S::kKeys], v_table[S::kRing][S::kKeys];
@@ -464,28 +467,49 @@ kvcache_attention_tile_kernel(const AttentionArgs a)
             load(v_next, v_from);
         };
 
-        // ---- the first tables, scales and rows
+        // ---- the first tables, scales and rows, each kind of read sent at once
         if (wave < 2) {
+            uint32_t ahead_raw[5];
+#pragma unroll
+            for (int i = 0; i < 5; ++i) {
+                look_up(i);
+                ahead_raw[i] = raw;
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                look_up(i);
+                raw = ahead_raw[i];
                 write_table(i);
             }
-            look_up(4);
+            raw = ahead_raw[4];
         } else if (H::coded && wave < 4) {
-            look_up(0);
+            uint32_t ahead_raw[3];
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                look_up(i);
+                ahead_raw[i] = raw;
+            }
+            raw = ahead_raw[0];
             load_scale(0);
-            write_scale(0);
-            look_up(1);
+            const float scale_0 = scale;
+            raw = ahead_raw[1];
             load_scale(1);
-            look_up(2);
+            const float scale_1 = scale;
+            scale = scale_0;
+            write_scale(0);
+            scale = scale_1;
+            raw = ahead_raw[2];
         }
         local_barrier();
-        find(-2);
-        load(k_next, k_from);
-        put_keys(0);
-        find(-1);
-        send();
+        {
+            Piece k_first[S::kPasses];
+            find(-2);
+            load(k_first, k_from);
+            find(-1);
+            send();
+#pragma unroll
+            for (int j = 0; j < S::kPasses; ++j)
+                *(u32x4 *)(k_lds[0] + (key0 + j * S::kRowsAtOnce) * S::kKStride + piece * 16) = H::key(k_first[j]);
+        }
         if (second) {
             put(0);
             find(0);
@@ -496,7 +520,7 @@ kvcache_attention_tile_kernel(const AttentionArgs a)
 
         // ---- the two blocks of work
         f32x16 s[S::kKeys / 32];
-        typename V::eight p[S::kKeys / 16];
+        typename V::eight p[S::kKeys / 16], rest[kTwice ? S::kKeys / 16 : 1];
         constexpr int kBlocks = S::kKeys / 32;
         const uint32_t k_lane = col * S::kKStride + half * 16;
         // of a block of 16 keys, keys 4 half .. + 3 and 8 + 4 half .. + 3
@@ -530,6 +554,8 @@ kvcache_attention_tile_kernel(const AttentionArgs a)
             find(second ? i + 2 : i + 1);
             feed.run([&](int n) { return read_v(i, n); }, [&](int n, typename V::eight v) {
                 o[n % (DP / 32)] = V::mfma32(v, p[n / (DP / 32)], o[n % (DP / 32)]);
+                if constexpr (kTwice)
+                    o[n % (DP / 32)] = V::mfma32(v, rest[n / (DP / 32)], o[n % (DP / 32)]);
             });
             if (on_edge(i) && __builtin_amdgcn_readfirstlane(special[i & (2 * S::kRing - 1)])) {
                 const int32_t t0 = lo + i * S::kKeys;
@@ -616,6 +642,13 @@ kvcache_attention_tile_kernel(const AttentionArgs a)
                 }
                 p[2 * b] = __builtin_bit_cast(typename V::eight, pack8<V>(w));
                 p[2 * b + 1] = __builtin_bit_cast(typename V::eight, pack8<V>(w + 8));
+                if constexpr (kTwice) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        w[j] = __builtin_isfinite(w[j]) ? w[j] - (float)p[2 * b + j / 8][j % 8] : 0.0f;
+                    rest[2 * b] = __builtin_bit_cast(typename V::eight, pack8<V>(w));
+                    rest[2 * b + 1] = __builtin_bit_cast(typename V::eight, pack8<V>(w + 8));
+                }
             }
         };
 
@@ -734,9 +767,13 @@ __global__ __launch_bounds__(64 * kSingleWaves, DP == 256 && (__is_same(F, void)
     // Without a window a split starts where it starts: its first lookup need
     // not wait for the sequence's length (what it gives is checked later).
     const int32_t mine = (int32_t)(lane % S::kKeys);   // the key of a step whose row this lane looks up
-    uint32_t raw = 0;
-    if (a.window == 0 && a.max_context > 0)
-        raw = raw_page(a, table, (int32_t)(split * a.split_keys + wave * S::kKeys) + mine, (int32_t)a.max_context);
+    uint32_t raw = 0, raw_1 = 0, raw_2 = 0;
+    if (a.window == 0 && a.max_context > 0) {
+        const int32_t t = (int32_t)(split * a.split_keys + wave * S::kKeys) + mine;
+        raw = raw_page(a, table, t, (int32_t)a.max_context);
+        raw_1 = raw_page(a, table, t + S::kKeys * kSingleWaves, (int32_t)a.max_context);
+        raw_2 = raw_page(a, table, t + 2 * S::kKeys * kSingleWaves, (int32_t)a.max_context);
+    }
     const Sequence seq = sequence_of(a, blockIdx.y);
     uint32_t rows = (uint32_t)seq.n * a.group.d;
     rows = rows < kSingleRows ? rows : kSingleRows;   // more: flagged by sequence_of
@@ -822,15 +859,20 @@ __global__ __launch_bounds__(64 * kSingleWaves, DP == 256 && (__is_same(F, void)
         const auto in_order = [] { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); };
         constexpr int kStep = S::kKeys * kSingleWaves;
         int32_t t0 = lo + (int32_t)wave * S::kKeys;
-        if (a.window > 0)
+        if (a.window > 0) {
+            look_up(t0 + kStep);
+            raw_1 = raw;
+            look_up(t0 + 2 * kStep);
+            raw_2 = raw;
             look_up(t0);
+        }
         put_table(t0);
         in_order();
         load_rows();
-        look_up(t0 + kStep);
         in_order();
+        raw = raw_1;
         put_table(t0 + kStep);
-        look_up(t0 + 2 * kStep);
+        raw = raw_2;
         for (; t0 < hi; t0 += kStep) {
             f32x4 s[S::kBlocks] = {};
 #pragma unroll

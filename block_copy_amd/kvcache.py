@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 import torch
 
@@ -77,6 +78,11 @@ class AttentionArgs(ctypes.Structure):
                 ("window", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
+# kvcache_rope_t in one call: a ctypes structure costs twice the time to fill.
+_PACK_ROPE = struct.Struct("@IIIfPPQIIII" + "Pqq" * 4).pack
+_ROPE_BYTES, _NO_ROWS = ctypes.sizeof(Rope), (0, 0, 0)
+
+
 def _declare():
     p, u32, u64 = ctypes.c_void_p, ctypes.c_uint32, ctypes.c_uint64
     pages, rows = ctypes.POINTER(Pages), ctypes.POINTER(Rows)
@@ -84,7 +90,7 @@ def _declare():
     lib.kvcache_rope_frequencies.argtypes = [p, u32, ctypes.c_double, ctypes.c_int, ctypes.c_double,
                                              u32, ctypes.c_double, ctypes.c_double]
     lib.kvcache_rope.restype = ctypes.c_int
-    lib.kvcache_rope.argtypes = [ctypes.POINTER(Rope), p]
+    lib.kvcache_rope.argtypes = [p, p]
     for f in (lib.kvcache_write, lib.kvcache_read):
         f.restype = ctypes.c_int
         f.argtypes = [pages, u32, rows, rows, p, u64, p, p]
@@ -147,7 +153,7 @@ def _rows(t, shape, dtype, device, what):
     if t.dtype != dtype or t.device != device or t.shape != shape or (st[2] != 1 and shape[2] != 1):
         raise ValueError(f"{what} must be {dtype} of shape {tuple(shape)} on {device}, "
                          "its last dimension contiguous")
-    return Rows(t.data_ptr(), st[0], st[1])
+    return t.data_ptr(), st[0], st[1]
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none",
@@ -174,25 +180,26 @@ def rope(positions, freqs, q, k=None, *, q_out=None, k_out=None, interleaved: bo
         raise ValueError("q must be a [tokens, heads, head_dim] bfloat16, float16 or float32 GPU tensor")
     tokens, heads, dim = shape
     pairs = freqs.shape[0]
-    a = Rope(ctypes.sizeof(Rope), _TYPES[dt],
-             (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0), factor)
-    a.positions = _vector(positions, torch.int32, tokens, dev, "positions")
-    a.freq = _vector(freqs, torch.float64, pairs, dev, "freqs")
-    a.tokens, a.head_dim, a.rot_dim, a.q_heads = tokens, dim, 2 * pairs, heads
     if q_out is None:
         q_out = torch.empty(shape, dtype=dt, device=dev)
-    a.q, a.q_out = _rows(q, shape, dt, dev, "q"), _rows(q_out, shape, dt, dev, "q_out")
+    k_heads, k_rows, k_out_rows = 0, _NO_ROWS, _NO_ROWS
     if k is not None:
         kshape = k.shape
         if len(kshape) != 3 or kshape[0] != tokens or kshape[2] != dim:
             raise ValueError("k must be [tokens, heads, head_dim], with q's tokens and head_dim")
         if k_out is None:
             k_out = torch.empty(kshape, dtype=dt, device=dev)
-        a.k_heads = kshape[1]
-        a.k, a.k_out = _rows(k, kshape, dt, dev, "k"), _rows(k_out, kshape, dt, dev, "k_out")
+        k_heads = kshape[1]
+        k_rows, k_out_rows = _rows(k, kshape, dt, dev, "k"), _rows(k_out, kshape, dt, dev, "k_out")
     elif k_out is not None:
         raise ValueError("k_out without k")
-    _call(lib.kvcache_rope, "kvcache_rope", dev, stream, ctypes.byref(a))
+    packed = _PACK_ROPE(_ROPE_BYTES, _TYPES[dt],
+                        (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0), factor,
+                        _vector(positions, torch.int32, tokens, dev, "positions"),
+                        _vector(freqs, torch.float64, pairs, dev, "freqs"),
+                        tokens, dim, 2 * pairs, heads, k_heads, *_rows(q, shape, dt, dev, "q"), *k_rows,
+                        *_rows(q_out, shape, dt, dev, "q_out"), *k_out_rows)
+    _call(lib.kvcache_rope, "kvcache_rope", dev, stream, packed)
     return q_out, k_out
 
 
@@ -234,7 +241,7 @@ def write(cache: PagedCache, k, v, slots, *, status=None, stream=None) -> None:
     if k.dim() != 3 or k.dtype not in _ROW_TYPES[:2]:
         raise ValueError("k must be a 3-dimensional bfloat16 or float16 tensor")
     dev, shape = cache.device, (k.shape[0], cache.kv_heads, cache.head_dim)
-    r, w = _rows(k, shape, k.dtype, dev, "k"), _rows(v, shape, k.dtype, dev, "v")
+    r, w = Rows(*_rows(k, shape, k.dtype, dev, "k")), Rows(*_rows(v, shape, k.dtype, dev, "v"))
     _call(lib.kvcache_write, "kvcache_write", dev, stream, cache._ref, _TYPES[k.dtype], ctypes.byref(r),
           ctypes.byref(w), _vector(slots, torch.int64, shape[0], dev, "slots"), shape[0], _status(status, dev))
 
@@ -254,7 +261,7 @@ def read(cache: PagedCache, slots, k_out=None, v_out=None, *, dtype=None, status
         k_out = torch.empty(shape, dtype=dtype, device=dev)
     if v_out is None:
         v_out = torch.empty(shape, dtype=dtype, device=dev)
-    r, w = _rows(k_out, shape, dtype, dev, "k_out"), _rows(v_out, shape, dtype, dev, "v_out")
+    r, w = Rows(*_rows(k_out, shape, dtype, dev, "k_out")), Rows(*_rows(v_out, shape, dtype, dev, "v_out"))
     _call(lib.kvcache_read, "kvcache_read", dev, stream, cache._ref, _TYPES[dtype], ctypes.byref(r),
           ctypes.byref(w), _vector(slots, torch.int64, shape[0], dev, "slots"), shape[0], _status(status, dev))
     return k_out, v_out
@@ -295,7 +302,7 @@ class AttentionPlan:
         a, dev = self.args, self.cache.device
         if out is None:
             out = torch.empty(self.shape, dtype=self.dtype, device=dev)
-        a.q = _rows(q, self.shape, self.dtype, dev, "q")
+        a.q = _rows(q, self.shape, self.dtype, dev, "q")       # a tuple fills the structure
         a.out = _rows(out, self.shape, self.dtype, dev, "out")
         ts, st = page_table.shape, page_table.stride()
         if (page_table.dtype != torch.int32 or page_table.device != dev or len(ts) != 2 or ts[0] != self.num_seqs

@@ -186,9 +186,10 @@ int kvcache_read(const kvcache_pages_t *pages, uint32_t dtype, const kvcache_row
  * One new token a sequence (a decode step), a few (a drafted continuation) and
  * long chunks go through the same call.
  *
- * Products are accumulated in 32 bits; softmax weights are rounded to 16 bits
- * before the second product (bf16, or fp16 when the pages are FP16), after
- * they were multiplied with the value's scale, while their sum is kept
+ * Products are accumulated in 32 bits.  Softmax weights, multiplied with the
+ * value's scale, are rounded before the second product: to fp16 where the pages
+ * are FP16, else to bf16, or to two bf16 parts (16 bits) for at most 16 rows a
+ * key/value head and for FP16 rows over 8-bit pages.  Their sum is kept
  * unrounded.  Results do not depend on the launch (no atomics).
  *
  * max_q_len and max_context bound the lengths (they shape the launch; a longer

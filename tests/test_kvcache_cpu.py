@@ -50,6 +50,11 @@ def test_binding_matches_the_compiled_header(C, tmp_path):
                                                               text=True).stdout.splitlines())
     for n in consts:
         assert getattr(C, n) == int(got[n]), n
+    # the packed form of kvcache_rope_t: the same bytes as the structure's
+    rows = [(10 + i, 20 + i, 30 + i) for i in range(4)]
+    flat = (C.ctypes.sizeof(C.Rope), 1, 2, 0.5, 77, 88, 9, 64, 32, 8, 2)
+    a = C.Rope(*flat, *[C.Rows(*r) for r in rows])
+    assert bytes(a) == C._PACK_ROPE(*flat, *[x for r in rows for x in r])
     for k in kinds:
         assert C.SCALINGS[k] == int(got["kind_" + k])
     for name, cls in structs.items():
