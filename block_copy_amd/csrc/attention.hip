@@ -27,6 +27,8 @@
 // loop adds them to the rows that see them (`add_special`).
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "cache_internal.h"
 #include "cache_types.h"
 
@@ -739,23 +741,26 @@ struct SingleShape {
     static constexpr int kVStride = DP * 2 + 32;   // 32 mod 256: see above, for blocks of 16 rows
     static constexpr int kVBytes = kKeys * kVStride;
     static constexpr int kWaveBytes = kVBytes + kKeys * (8 + 16);   // and the scales and addresses
-    static constexpr int kPieces = DP / 8;
-    static constexpr int kRowsAtOnce = 64 / kPieces;
-    static constexpr int kPasses = kKeys / kRowsAtOnce;
     static constexpr int kBlocks = kKeys / 16;     // of the first product
     static constexpr int kPairs = kKeys / 32;      // and of the second
     static constexpr int kJoinBytes = kSingleWaves * kSingleRows * (DP + 4) * 4;
     static constexpr int kBytes = kSingleWaves * kWaveBytes > kJoinBytes ? kSingleWaves * kWaveBytes : kJoinBytes;
 };
 
-// Full: head_dim is DP, and no piece lies behind a row's end.
+// Full: head_dim is DP, so no piece lies behind a row's end, and 8-bit rows can
+// be read 16 codes to a lane: of a row's 64 codes, one read takes all, where
+// two reads of 8 codes a lane look the same line up twice.
 template <class T, class F, int DP, bool Full>
 __global__ __launch_bounds__(64 * kSingleWaves, DP == 256 && (__is_same(F, void) || !Full) ? 1 : 2) void kvcache_attention_single_kernel(const AttentionArgs a)
 {
     typedef Held<T, F> H;
     typedef SingleShape<H, DP> S;
     typedef typename H::V V;
-    typedef typename H::piece Piece;
+    constexpr bool kWide = Full && H::coded;
+    constexpr int kPieceEights = kWide ? 2 : 1;
+    typedef std::conditional_t<kWide, u32x4, typename H::piece> Piece;
+    constexpr int kPieces = DP / (8 * kPieceEights);   // of a row
+    constexpr int kRowsAtOnce = 64 / kPieces, kPasses = S::kKeys / kRowsAtOnce;
     constexpr bool kTwice = __is_same(V, Bf16);
     __shared__ __align__(16) uint8_t lds[S::kBytes];
     __shared__ float join_m[kSingleWaves][kSingleRows], join_l[kSingleWaves][kSingleRows];
@@ -805,7 +810,7 @@ __global__ __launch_bounds__(64 * kSingleWaves, DP == 256 && (__is_same(F, void)
                                        (int64_t)(head * a.group.d + member) * a.q_sh;
 #pragma unroll
         for (int s = 0; s < DP / 32; ++s) {
-            const uint32_t d = s * 32 + group * 8;
+            const uint32_t d = kWide ? s / 2 * 64 + group * 16 + s % 2 * 8 : s * 32 + group * 8;
             u32x4 p = {};
             if (held && (Full || d < a.head_dim))
                 p = (*(const u32x4 *)(q_at + d) & a.q_keep) ^ a.q_flip;
@@ -813,8 +818,8 @@ __global__ __launch_bounds__(64 * kSingleWaves, DP == 256 && (__is_same(F, void)
         }
 
         const uint32_t esize = H::coded ? 1 : 2;
-        const uint32_t piece = lane % S::kPieces, vkey = lane / S::kPieces;
-        Piece kp[S::kBlocks][DP / 32], vp[S::kPasses];
+        const uint32_t piece = lane % kPieces, vkey = lane / kPieces;
+        Piece kp[S::kBlocks][DP / 32 / kPieceEights], vp[kPasses];
         uint64_t k_scale_at, v_scale_at;
         float k_scale = 0.0f, v_scale = 0.0f;
         const uint8_t *k_base = (const uint8_t *)a.k + (int64_t)head * a.k_head * esize;
@@ -840,17 +845,31 @@ __global__ __launch_bounds__(64 * kSingleWaves, DP == 256 && (__is_same(F, void)
             }
 #pragma unroll
             for (int b = 0; b < S::kBlocks; ++b) {
-                const uint64_t at = addresses[b * 16 + col] + group * 8 * esize;
+                const uint64_t at = addresses[b * 16 + col] + group * sizeof(Piece);
 #pragma unroll
-                for (int s = 0; s < DP / 32; ++s)
-                    kp[b][s] = load_at<Piece>(Full || s * 32 + group * 8 < a.head_dim ? at + s * 32 * esize
+                for (int s = 0; s < DP / 32 / kPieceEights; ++s)
+                    kp[b][s] = load_at<Piece>(Full || s * 32 + group * 8 < a.head_dim ? at + s * 4 * sizeof(Piece)
                                                                                      : (uint64_t)kZeros);
             }
 #pragma unroll
-            for (int i = 0; i < S::kPasses; ++i) {
-                const uint64_t at = addresses[S::kKeys + i * S::kRowsAtOnce + vkey] + piece * 8 * esize;
+            for (int i = 0; i < kPasses; ++i) {
+                const uint64_t at = addresses[S::kKeys + i * kRowsAtOnce + vkey] + piece * sizeof(Piece);
                 vp[i] = load_at<Piece>(Full || piece * 8 < a.head_dim ? at : (uint64_t)kZeros);
             }
+        };
+
+        // Eight of a piece, as the products take them.
+        const auto key_of = [&](int b, int i) {
+            if constexpr (kWide)
+                return H::key(i % 2 ? u32x2{kp[b][i / 2].z, kp[b][i / 2].w} : u32x2{kp[b][i / 2].x, kp[b][i / 2].y});
+            else
+                return H::key(kp[b][i]);
+        };
+        const auto value_of = [&](int i, int e) {
+            if constexpr (kWide)
+                return H::value(e ? u32x2{vp[i].z, vp[i].w} : u32x2{vp[i].x, vp[i].y});
+            else
+                return H::value(vp[i]);
         };
 
         // A wavefront's own writes to shared memory are read by other lanes of
@@ -879,7 +898,7 @@ __global__ __launch_bounds__(64 * kSingleWaves, DP == 256 && (__is_same(F, void)
             for (int i = 0; i < DP / 32; ++i)
 #pragma unroll
                 for (int b = 0; b < S::kBlocks; ++b)
-                    s[b] = T::mfma16(__builtin_bit_cast(typename T::eight, H::key(kp[b][i])), q[i], s[b]);
+                    s[b] = T::mfma16(__builtin_bit_cast(typename T::eight, key_of(b, i)), q[i], s[b]);
             if (H::coded) {
                 scales[mine] = k_scale;
                 scales[S::kKeys + mine] = v_scale;
@@ -888,22 +907,24 @@ __global__ __launch_bounds__(64 * kSingleWaves, DP == 256 && (__is_same(F, void)
             const bool edge = t0 + S::kKeys - 1 > first || t0 + S::kKeys > hi ||
                               (a.window > 0 && t0 <= last - a.window);
             bool special = false;
-            u32x4 values[S::kPasses];
+            constexpr int kEights = kPasses * kPieceEights;
+            u32x4 values[kEights];
 #pragma unroll
-            for (int i = 0; i < S::kPasses; ++i)
-                values[i] = H::value(vp[i]);
+            for (int i = 0; i < kEights; ++i)
+                values[i] = value_of(i / kPieceEights, i % kPieceEights);
             if (!H::coded && kTwice)
-                special = __builtin_amdgcn_ballot_w64(any_special<V, S::kPasses>(values)) != 0;
+                special = __builtin_amdgcn_ballot_w64(any_special<V, kEights>(values)) != 0;
             if (special || edge) {
                 special = false;
 #pragma unroll
-                for (int i = 0; i < S::kPasses; ++i)
+                for (int i = 0; i < kEights; ++i)
                     special |= clean<V>(values[i]);
                 special = __builtin_amdgcn_ballot_w64(special) != 0;
             }
 #pragma unroll
-            for (int i = 0; i < S::kPasses; ++i)
-                *(u32x4 *)(vlds + (i * S::kRowsAtOnce + vkey) * S::kVStride + piece * 16) = values[i];
+            for (int i = 0; i < kEights; ++i)
+                *(u32x4 *)(vlds + (i / kPieceEights * kRowsAtOnce + vkey) * S::kVStride +
+                           (piece * kPieceEights + i % kPieceEights) * 16) = values[i];
             in_order();
             load_rows();   // of the next step: zeros behind the last key
 
@@ -1181,13 +1202,13 @@ __global__ __launch_bounds__(kJoinThreads) void kvcache_attention_join_kernel(co
 template <class T, class F, int DP>
 void attention_pick(const AttentionArgs &a, const AttentionShape &shape, uint32_t num_seqs, hipStream_t s)
 {
-    if (shape.single && a.head_dim == DP)
+    if (shape.single && a.full)
         hipLaunchKernelGGL((kvcache_attention_single_kernel<T, F, DP, true>), dim3(a.kv_heads * a.splits, num_seqs),
                            dim3(64 * kSingleWaves), 0, s, a);
     else if (shape.single)
         hipLaunchKernelGGL((kvcache_attention_single_kernel<T, F, DP, false>), dim3(a.kv_heads * a.splits, num_seqs),
                            dim3(64 * kSingleWaves), 0, s, a);
-    else if (a.head_dim == DP)
+    else if (a.full)
         hipLaunchKernelGGL((kvcache_attention_tile_kernel<T, F, DP, true>),
                            dim3(a.kv_heads * a.splits * a.tiles, num_seqs), dim3(TileShape<DP>::kThreads), 0, s, a);
     else

@@ -325,6 +325,11 @@ extern "C" int kvcache_attention(const kvcache_pages_t *p, const kvcache_attenti
     a.q_heads = g->q_heads;
     a.kv_heads = p->kv_heads;
     a.head_dim = p->head_dim;
+    a.full = p->head_dim == 64 || p->head_dim == 128 || p->head_dim == 256;
+    if (element_bytes(p->format) == 1)
+        for (int i = 0; i < 3; ++i)
+            a.full = a.full && aligned(p->k, 16) && aligned(p->v, 16) && p->k_stride[i] % 16 == 0 &&
+                     p->v_stride[i] % 16 == 0;
     a.tiles = shape.tiles;
     a.splits = shape.splits;
     a.split_keys = shape.split_keys;

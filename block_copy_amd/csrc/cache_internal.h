@@ -55,6 +55,7 @@ struct AttentionArgs {
     float *part_o, *part_ml;   // [split][token][head][head_dim], [split][token][head][2]
     uint32_t num_pages, total_q, max_q_len, max_context;
     uint32_t q_heads, kv_heads, head_dim;
+    uint32_t full;             // head_dim is 64, 128 or 256, and 8-bit rows can be read 16 codes at once
     uint32_t tiles, splits, split_keys;
     int32_t window;
     float scale_log2;          // |scale| * log2(e), or 1 where scale is 0

@@ -289,6 +289,8 @@ CASES = [
     _case(q_lens=[50, 20], ctx=[30, 20], heads=2, kv=1, dim=40, page=16),  # rows before the first key
     _case(q_lens=[20], ctx=[555], heads=32, kv=1, dim=64, page=64, window=1),
     _case(q_lens=[1], ctx=[700], heads=32, kv=1, dim=192, page=16),        # one token, many heads
+    _case(q_lens=[1, 2], ctx=[333, 70], heads=4, kv=2, dim=128, pad=8),    # 8-bit rows 8 bytes apart from 16
+    _case(q_lens=[40], ctx=[140], heads=4, kv=2, dim=64, pad=8),
 ]
 
 
