@@ -639,7 +639,7 @@ kvcache_attention_tile_kernel(const AttentionArgs a)
                         // a hidden row's scale may be anything
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            w[4 * j + e] = w[4 * j + e] == 0.0f ? 0.0f : w[4 * j + e] * c[e];
+                            w[4 * j + e] = s[b][4 * j + e] == -__builtin_inff() ? 0.0f : w[4 * j + e] * c[e];
                     }
                 }
                 p[2 * b] = __builtin_bit_cast(typename V::eight, pack8<V>(w));
@@ -976,7 +976,7 @@ __global__ __launch_bounds__(64 * kSingleWaves, DP == 256 && (__is_same(F, void)
                         // a hidden row's scale may be anything
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            w[4 * b + j] = w[4 * b + j] == 0.0f ? 0.0f : w[4 * b + j] * c[j];
+                            w[4 * b + j] = s[2 * i + b][j] == -__builtin_inff() ? 0.0f : w[4 * b + j] * c[j];
                     }
                 }
                 p[i] = __builtin_bit_cast(typename V::eight, pack8<V>(w));
@@ -1200,54 +1200,42 @@ __global__ __launch_bounds__(kJoinThreads) void kvcache_attention_join_kernel(co
 }
 
 template <class T, class F, int DP>
-void attention_pick(const AttentionArgs &a, const AttentionShape &shape, uint32_t num_seqs, hipStream_t s)
+hipError_t attention_pick(const AttentionArgs &a, const AttentionShape &shape, uint32_t num_seqs, hipStream_t s)
 {
-    if (shape.single && a.full)
-        hipLaunchKernelGGL((kvcache_attention_single_kernel<T, F, DP, true>), dim3(a.kv_heads * a.splits, num_seqs),
-                           dim3(64 * kSingleWaves), 0, s, a);
-    else if (shape.single)
-        hipLaunchKernelGGL((kvcache_attention_single_kernel<T, F, DP, false>), dim3(a.kv_heads * a.splits, num_seqs),
-                           dim3(64 * kSingleWaves), 0, s, a);
-    else if (a.full)
-        hipLaunchKernelGGL((kvcache_attention_tile_kernel<T, F, DP, true>),
-                           dim3(a.kv_heads * a.splits * a.tiles, num_seqs), dim3(TileShape<DP>::kThreads), 0, s, a);
-    else
-        hipLaunchKernelGGL((kvcache_attention_tile_kernel<T, F, DP, false>),
-                           dim3(a.kv_heads * a.splits * a.tiles, num_seqs), dim3(TileShape<DP>::kThreads), 0, s, a);
+    const uint32_t blocks = a.kv_heads * a.splits * a.tiles;
+    if (shape.single)
+        return launch(a.full ? kvcache_attention_single_kernel<T, F, DP, true>
+                             : kvcache_attention_single_kernel<T, F, DP, false>,
+                      blocks, num_seqs, 64 * kSingleWaves, a, s);
+    return launch(a.full ? kvcache_attention_tile_kernel<T, F, DP, true> : kvcache_attention_tile_kernel<T, F, DP, false>,
+                  blocks, num_seqs, TileShape<DP>::kThreads, a, s);
 }
 
 template <class T, class F>
-void attention_dim(const AttentionArgs &a, const AttentionShape &shape, uint32_t num_seqs, hipStream_t s)
+hipError_t attention_dim(const AttentionArgs &a, const AttentionShape &shape, uint32_t num_seqs, hipStream_t s)
 {
     if (a.head_dim <= 64)
-        attention_pick<T, F, 64>(a, shape, num_seqs, s);
-    else if (a.head_dim <= 128)
-        attention_pick<T, F, 128>(a, shape, num_seqs, s);
-    else
-        attention_pick<T, F, 256>(a, shape, num_seqs, s);
+        return attention_pick<T, F, 64>(a, shape, num_seqs, s);
+    if (a.head_dim <= 128)
+        return attention_pick<T, F, 128>(a, shape, num_seqs, s);
+    return attention_pick<T, F, 256>(a, shape, num_seqs, s);
 }
 
 template <class T>
 hipError_t attention_type(const AttentionArgs &a, const AttentionShape &shape, uint32_t num_seqs,
                           uint32_t format, hipStream_t s)
 {
-    if (format == KVCACHE_FP8)
-        attention_dim<T, Fp8>(a, shape, num_seqs, s);
-    else if (format == KVCACHE_INT8)
-        attention_dim<T, Int8>(a, shape, num_seqs, s);
-    else
-        attention_dim<T, void>(a, shape, num_seqs, s);
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = format == KVCACHE_FP8    ? attention_dim<T, Fp8>(a, shape, num_seqs, s)
+                         : format == KVCACHE_INT8 ? attention_dim<T, Int8>(a, shape, num_seqs, s)
+                                                  : attention_dim<T, void>(a, shape, num_seqs, s);
     if (e != hipSuccess || a.splits == 1)
         return e;
     const uint64_t rows = (uint64_t)a.total_q * a.q_heads;
     const uint32_t at_once = kJoinThreads / (a.head_dim / 4);
     if (a.splits <= kFewSplits)
-        hipLaunchKernelGGL((kvcache_attention_join_few_kernel<T>), dim3((uint32_t)((rows + at_once - 1) / at_once)),
-                           dim3(kJoinThreads), 0, s, a);
-    else
-        hipLaunchKernelGGL((kvcache_attention_join_kernel<T>), dim3((uint32_t)rows), dim3(kJoinThreads), 0, s, a);
-    return hipGetLastError();
+        return launch(kvcache_attention_join_few_kernel<T>, (uint32_t)((rows + at_once - 1) / at_once), 1,
+                      kJoinThreads, a, s);
+    return launch(kvcache_attention_join_kernel<T>, (uint32_t)rows, 1, kJoinThreads, a, s);
 }
 
 }  // namespace

@@ -70,6 +70,17 @@ struct AttentionShape {
     uint64_t workspace_bytes;
 };
 
+// One kernel whose only argument is `a`.  (The launch's own result, not the
+// thread's last error, which may be an earlier call's.)
+template <class A>
+hipError_t launch(void (*kernel)(const A), uint32_t grid_x, uint32_t grid_y, uint32_t threads, const A &a,
+                  hipStream_t stream)
+{
+    void *args[] = {const_cast<A *>(&a)};
+    return hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3(grid_x, grid_y), dim3(threads), args, 0,
+                           stream);
+}
+
 hipError_t launch_rope(const RopeArgs &a, uint32_t dtype, bool wide, hipStream_t stream);
 hipError_t launch_write(const RowArgs &a, uint32_t dtype, uint32_t format, bool wide, hipStream_t stream);
 hipError_t launch_read(const RowArgs &a, uint32_t dtype, uint32_t format, bool wide, hipStream_t stream);

@@ -374,73 +374,71 @@ uint32_t blocks_for(uint64_t items, uint32_t per_block)
 }
 
 template <class T>
-void rope_pick(const RopeArgs &a, bool wide, uint32_t blocks, hipStream_t s)
+hipError_t rope_pick(const RopeArgs &a, bool wide, uint32_t blocks, hipStream_t s)
 {
-    const dim3 g(blocks), t(kThreads);
     if (wide && a.interleaved)
-        hipLaunchKernelGGL((kvcache_rope_kernel<T, true, true>), g, t, 0, s, a);
-    else if (wide)
-        hipLaunchKernelGGL((kvcache_rope_kernel<T, true, false>), g, t, 0, s, a);
-    else if (a.interleaved)
-        hipLaunchKernelGGL((kvcache_rope_kernel<T, false, true>), g, t, 0, s, a);
-    else
-        hipLaunchKernelGGL((kvcache_rope_kernel<T, false, false>), g, t, 0, s, a);
+        return launch(kvcache_rope_kernel<T, true, true>, blocks, 1, kThreads, a, s);
+    if (wide)
+        return launch(kvcache_rope_kernel<T, true, false>, blocks, 1, kThreads, a, s);
+    if (a.interleaved)
+        return launch(kvcache_rope_kernel<T, false, true>, blocks, 1, kThreads, a, s);
+    return launch(kvcache_rope_kernel<T, false, false>, blocks, 1, kThreads, a, s);
 }
 
 template <class T, class Format>
-void write_pick(const RowArgs &a, bool wide, hipStream_t s)
+hipError_t write_pick(const RowArgs &a, bool wide, hipStream_t s)
 {
     const uint64_t rows = (uint64_t)a.tokens * a.kv_heads.d;
-    const dim3 t(kThreads);
+    const auto go = [&](void (*kernel)(const RowArgs), uint32_t lanes) {
+        return launch(kernel, blocks_for(rows, kThreads / lanes), 1, kThreads, a, s);
+    };
     if (!wide)
-        hipLaunchKernelGGL((kvcache_write_any_kernel<T, Format>), dim3(blocks_for(rows, kThreads / 64)), t, 0, s, a);
-    else if (a.head_dim <= 64)
-        hipLaunchKernelGGL((kvcache_write_kernel<T, Format, 8>), dim3(blocks_for(rows, kThreads / 8)), t, 0, s, a);
-    else if (a.head_dim <= 128)
-        hipLaunchKernelGGL((kvcache_write_kernel<T, Format, 16>), dim3(blocks_for(rows, kThreads / 16)), t, 0, s, a);
-    else if (a.head_dim <= 256)
-        hipLaunchKernelGGL((kvcache_write_kernel<T, Format, 32>), dim3(blocks_for(rows, kThreads / 32)), t, 0, s, a);
-    else
-        hipLaunchKernelGGL((kvcache_write_kernel<T, Format, 64>), dim3(blocks_for(rows, kThreads / 64)), t, 0, s, a);
+        return go(kvcache_write_any_kernel<T, Format>, 64);
+    if (a.head_dim <= 64)
+        return go(kvcache_write_kernel<T, Format, 8>, 8);
+    if (a.head_dim <= 128)
+        return go(kvcache_write_kernel<T, Format, 16>, 16);
+    if (a.head_dim <= 256)
+        return go(kvcache_write_kernel<T, Format, 32>, 32);
+    return go(kvcache_write_kernel<T, Format, 64>, 64);
 }
 
 template <class S, class T>
-void read_pick(const RowArgs &a, bool wide, hipStream_t s)
+hipError_t read_pick(const RowArgs &a, bool wide, hipStream_t s)
 {
     const uint64_t rows = (uint64_t)a.tokens * a.kv_heads.d;
-    const dim3 t(kThreads);
+    const auto go = [&](void (*kernel)(const RowArgs), uint32_t lanes) {
+        return launch(kernel, blocks_for(rows, kThreads / lanes), 1, kThreads, a, s);
+    };
     if (!wide)
-        hipLaunchKernelGGL((kvcache_read_any_kernel<S, T>), dim3(blocks_for(rows, kThreads / 64)), t, 0, s, a);
-    else if (a.head_dim <= 64)
-        hipLaunchKernelGGL((kvcache_read_kernel<S, T, 8>), dim3(blocks_for(rows, kThreads / 8)), t, 0, s, a);
-    else if (a.head_dim <= 128)
-        hipLaunchKernelGGL((kvcache_read_kernel<S, T, 16>), dim3(blocks_for(rows, kThreads / 16)), t, 0, s, a);
-    else if (a.head_dim <= 256)
-        hipLaunchKernelGGL((kvcache_read_kernel<S, T, 32>), dim3(blocks_for(rows, kThreads / 32)), t, 0, s, a);
-    else
-        hipLaunchKernelGGL((kvcache_read_kernel<S, T, 64>), dim3(blocks_for(rows, kThreads / 64)), t, 0, s, a);
+        return go(kvcache_read_any_kernel<S, T>, 64);
+    if (a.head_dim <= 64)
+        return go(kvcache_read_kernel<S, T, 8>, 8);
+    if (a.head_dim <= 128)
+        return go(kvcache_read_kernel<S, T, 16>, 16);
+    if (a.head_dim <= 256)
+        return go(kvcache_read_kernel<S, T, 32>, 32);
+    return go(kvcache_read_kernel<S, T, 64>, 64);
 }
 
 template <class S>
-void read_type(const RowArgs &a, uint32_t dtype, bool wide, hipStream_t s)
+hipError_t read_type(const RowArgs &a, uint32_t dtype, bool wide, hipStream_t s)
 {
     if (dtype == KVCACHE_BF16)
-        read_pick<S, Bf16>(a, wide, s);
-    else if (dtype == KVCACHE_FP16)
-        read_pick<S, Fp16>(a, wide, s);
-    else
-        read_pick<S, Fp32>(a, wide, s);
+        return read_pick<S, Bf16>(a, wide, s);
+    if (dtype == KVCACHE_FP16)
+        return read_pick<S, Fp16>(a, wide, s);
+    return read_pick<S, Fp32>(a, wide, s);
 }
 
 template <class T>
-void write_format(const RowArgs &a, uint32_t format, bool wide, hipStream_t s)
+hipError_t write_format(const RowArgs &a, uint32_t format, bool wide, hipStream_t s)
 {
     if (format == KVCACHE_FP8)
-        write_pick<T, Fp8>(a, wide, s);
-    else if (format == KVCACHE_INT8)
-        write_pick<T, Int8>(a, wide, s);
-    else
-        write_pick<T, void>(a, wide, s);
+        return write_pick<T, Fp8>(a, wide, s);
+    if (format == KVCACHE_INT8)
+        return write_pick<T, Int8>(a, wide, s);
+    return write_pick<T, void>(a, wide, s);
 }
 
 }  // namespace
@@ -458,34 +456,28 @@ hipError_t launch_rope(const RopeArgs &args, uint32_t dtype, bool wide, hipStrea
         a.block_tokens /= 2;
     const uint32_t blocks = blocks_for(a.tokens, a.block_tokens);
     if (dtype == KVCACHE_BF16)
-        rope_pick<Bf16>(a, wide, blocks, stream);
-    else if (dtype == KVCACHE_FP16)
-        rope_pick<Fp16>(a, wide, blocks, stream);
-    else
-        rope_pick<Fp32>(a, wide, blocks, stream);
-    return hipGetLastError();
+        return rope_pick<Bf16>(a, wide, blocks, stream);
+    if (dtype == KVCACHE_FP16)
+        return rope_pick<Fp16>(a, wide, blocks, stream);
+    return rope_pick<Fp32>(a, wide, blocks, stream);
 }
 
 hipError_t launch_write(const RowArgs &a, uint32_t dtype, uint32_t format, bool wide, hipStream_t stream)
 {
     if (dtype == KVCACHE_BF16)
-        write_format<Bf16>(a, format, wide, stream);
-    else
-        write_format<Fp16>(a, format, wide, stream);
-    return hipGetLastError();
+        return write_format<Bf16>(a, format, wide, stream);
+    return write_format<Fp16>(a, format, wide, stream);
 }
 
 hipError_t launch_read(const RowArgs &a, uint32_t dtype, uint32_t format, bool wide, hipStream_t stream)
 {
     if (format == KVCACHE_FP8)
-        read_type<Fp8>(a, dtype, wide, stream);
-    else if (format == KVCACHE_INT8)
-        read_type<Int8>(a, dtype, wide, stream);
-    else if (format == KVCACHE_BF16)
-        read_type<Bf16>(a, dtype, wide, stream);
-    else
-        read_type<Fp16>(a, dtype, wide, stream);
-    return hipGetLastError();
+        return read_type<Fp8>(a, dtype, wide, stream);
+    if (format == KVCACHE_INT8)
+        return read_type<Int8>(a, dtype, wide, stream);
+    if (format == KVCACHE_BF16)
+        return read_type<Bf16>(a, dtype, wide, stream);
+    return read_type<Fp16>(a, dtype, wide, stream);
 }
 
 }  // namespace kvc

@@ -218,17 +218,16 @@ class PagedCache:
         coded = k.dtype in (torch.float8_e4m3fn, torch.int8)
         _require(coded == (k_scales is not None) and coded == (v_scales is not None),
                  "8-bit pages need k_scales and v_scales, others take none")
-        p = Pages(ctypes.sizeof(Pages), _TYPES[k.dtype], k.data_ptr(), v.data_ptr())
-        for x, name in ((k, "k_stride"), (v, "v_stride")):
-            _require(x.stride(3) == 1 or x.shape[3] == 1, "head_dim must be contiguous")
-            setattr(p, name, _S3(*x.stride()[:3]))
+        ks, vs, dim = k.stride(), v.stride(), k.shape[3]
+        _require((ks[3] == 1 and vs[3] == 1) or dim == 1, "head_dim must be contiguous")
+        scales = [None, None, (0, 0, 0), (0, 0, 0)]
         if coded:
-            for x, name in ((k_scales, "ks_stride"), (v_scales, "vs_stride")):
+            for x in (k_scales, v_scales):
                 _require(x.shape == k.shape[:3] and x.dtype == torch.float32 and x.device == k.device,
                          "scales must be float32 of shape [num_pages, kv_heads, page_size]")
-                setattr(p, name, _S3(*x.stride()))
-            p.k_scale, p.v_scale = k_scales.data_ptr(), v_scales.data_ptr()
-        p.num_pages, p.kv_heads, p.page_size, p.head_dim = k.shape
+            scales = [k_scales.data_ptr(), v_scales.data_ptr(), k_scales.stride(), v_scales.stride()]
+        p = Pages(ctypes.sizeof(Pages), _TYPES[k.dtype], k.data_ptr(), v.data_ptr(), scales[0], scales[1],
+                  ks[:3], vs[:3], scales[2], scales[3], *k.shape)
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
         self.dtype, self.device, self.coded = k.dtype, k.device, coded
         self.num_pages, self.kv_heads, self.page_size, self.head_dim = k.shape

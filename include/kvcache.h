@@ -151,8 +151,8 @@ int kvcache_rope(const kvcache_rope_t *args, hipStream_t stream);
  * back as NaN.
  * errors: KVCOPY_EINVAL (struct_size; format or dtype unknown, 16-bit pages
  * of another dtype; NULL pointers; a zero size; head_dim above
- * KVCACHE_MAX_HEAD_DIM; kv_heads above 2^16; num_pages * page_size or tokens
- * >= 2^31), KVCOPY_EALIGN (a pointer not aligned to its element),
+ * KVCACHE_MAX_HEAD_DIM; kv_heads above 2^16; num_pages * page_size or tokens *
+ * kv_heads >= 2^31), KVCOPY_EALIGN (a pointer not aligned to its element),
  * KVCOPY_EHIP.
  */
 int kvcache_write(const kvcache_pages_t *pages, uint32_t dtype, const kvcache_rows_t *k,
@@ -194,7 +194,7 @@ int kvcache_read(const kvcache_pages_t *pages, uint32_t dtype, const kvcache_row
  *
  * max_q_len and max_context bound the lengths (they shape the launch; a longer
  * sequence sets KVCACHE_BAD_LENGTH, and what lies beyond the bound is neither
- * computed nor seen).  The workspace, kvcache_attention_workspace_bytes of the
+ * computed nor seen; rows of out that no sequence covers are undefined).  The workspace, kvcache_attention_workspace_bytes of the
  * same structures (it depends on the sizes alone, and may be 0), is scratch
  * for one call at a time.
  * errors: KVCOPY_EINVAL (struct_size; dtype not BF16 or FP16, or 16-bit pages

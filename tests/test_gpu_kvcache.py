@@ -374,6 +374,18 @@ def test_seen_infinities(C, q_len, kind):
     assert (o[..., 5] == math.inf).all() and (o[..., 6] == -math.inf).all() and o[..., 7:9].isnan().all()
 
 
+@pytest.mark.parametrize("kind", [F8, I8])
+@pytest.mark.parametrize("q_len", [1, 40])
+def test_seen_scales_of_nan(C, q_len, kind):
+    """A value that reads as NaN reaches every row that sees it, however small
+    its weight: here each row's weight for it is 0 or 1."""
+    def spoil(kp, vp, table, ks, vs):
+        at = int(table[0][1])
+        ks[at, :, 3], vs[at, :, 3] = 1e4, math.nan
+    c = _case(q_lens=[q_len], ctx=[400], heads=4, kv=1, dim=64, page=16, dtype=BF, kind=kind)
+    assert _attend(C, torch.Generator().manual_seed(5), edit=spoil, **c)["out"].isnan().all()
+
+
 @pytest.mark.parametrize("q_len", [1, 40])
 def test_extreme_scores(C, q_len):
     """Large scores of both signs: the running maximum grows and shrinks."""
