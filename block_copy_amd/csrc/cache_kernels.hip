@@ -20,7 +20,10 @@ constexpr uint32_t kMaxBlocks = 1u << 22;
 // sines, one pair a thread, into shared memory, and then turns all heads with
 // them, so the angle (a product and a reduction to one turn in 64 bits, since
 // a position of 2^20 has lost 2^-4 radians in 32) costs little beside the
-// heads' traffic.
+// heads' traffic.  The rows are read past the caches (their last use: 64.2
+// against 66.6 us for 16,384 tokens of 32 + 8 heads of 128 in bf16, 5.2 TB/s of
+// reads and writes, where a large copy reaches 4.9); the results, used next, go
+// through them.
 
 struct Turn {
     float c, s;
@@ -87,18 +90,18 @@ __global__ __launch_bounds__(kThreads) void kvcache_rope_kernel(const RopeArgs r
                 float x[8], y[8];
                 if (c >= turned) {
                     const uint32_t at = r.rot_dim + (c - turned) * 8;
-                    *(P *)(out + at) = *(const P *)(in + at);
+                    *(P *)(out + at) = load_once((const P *)(in + at));
                 } else if (Interleaved) {
                     const Turn *w = turns + t * half + c * 4;
-                    unpack8<T>(*(const P *)(in + c * 8), x);
+                    unpack8<T>(load_once((const P *)(in + c * 8)), x);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         rotate(x[2 * j], x[2 * j + 1], w[j]);
                     *(P *)(out + c * 8) = pack8<T>(x);
                 } else {
                     const Turn *w = turns + t * half + c * 8;
-                    unpack8<T>(*(const P *)(in + c * 8), x);
-                    unpack8<T>(*(const P *)(in + half + c * 8), y);
+                    unpack8<T>(load_once((const P *)(in + c * 8)), x);
+                    unpack8<T>(load_once((const P *)(in + half + c * 8)), y);
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         rotate(x[j], y[j], w[j]);
@@ -164,7 +167,9 @@ __device__ __forceinline__ float value_of(uint32_t bits)
 
 // kvcache_write: `Lanes` lanes share a row of keys and the same row of values,
 // a 16-byte piece each; a row's largest magnitude goes over them in log2(Lanes)
-// exchanges.  Format void: the pages hold T itself.
+// exchanges.  Format void: the pages hold T itself.  Bound by memory: 32,768
+// tokens of 8 heads of 128, bf16 to e4m3, in 40 us, 5.1 TB/s of reads and
+// writes.
 template <class T, class Format, int Lanes>
 __global__ __launch_bounds__(kThreads) void kvcache_write_kernel(const RowArgs a)
 {
@@ -273,7 +278,10 @@ __global__ __launch_bounds__(kThreads) void kvcache_write_any_kernel(const RowAr
 
 // ---- rows back from pages ---------------------------------------------------
 
-// S: what the pages hold (Bf16, Fp16, Fp8, Int8); T: the output's type.
+// kvcache_read: lanes share rows as in kvcache_write.  Both sides pass the
+// caches by: the rows are read back in bulk, for a connector or another
+// process (65,536 tokens of 8 heads of 128, int8 to bf16: 75.8 us, against
+// 84.7 us without).  S: what the pages hold; T: the output's type.
 template <class S>
 struct IsCode {
     static constexpr bool value = __is_same(S, Fp8) || __is_same(S, Int8);
@@ -302,7 +310,7 @@ __global__ __launch_bounds__(kThreads) void kvcache_read_kernel(const RowArgs a)
             float x[8] = {};
             if constexpr (IsCode<S>::value) {
                 if (slot >= 0) {
-                    const u32x2 c = *(const u32x2 *)((const uint8_t *)a.pages[i] + at);
+                    const u32x2 c = load_once((const u32x2 *)((const uint8_t *)a.pages[i] + at));
                     const float scale = a.scale[i][page_offset(page, place, a.s_page[i], a.s_place[i]) +
                                                    head * a.s_head[i]];
                     S::value4(c.x, x);
@@ -313,17 +321,17 @@ __global__ __launch_bounds__(kThreads) void kvcache_read_kernel(const RowArgs a)
                 }
                 out[i] = pack8<T>(x);
             } else if constexpr (__is_same(S, T)) {
-                out[i] = slot >= 0 ? *(const u32x4 *)((const typename S::elem *)a.pages[i] + at) : u32x4{};
+                out[i] = slot >= 0 ? load_once((const u32x4 *)((const typename S::elem *)a.pages[i] + at)) : u32x4{};
             } else {
                 if (slot >= 0)
-                    unpack8<S>(*(const u32x4 *)((const typename S::elem *)a.pages[i] + at), x);
+                    unpack8<S>(load_once((const u32x4 *)((const typename S::elem *)a.pages[i] + at)), x);
                 out[i] = pack8<T>(x);
             }
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            *(typename T::piece *)((typename T::elem *)a.rows[i] + token * a.r_token[i] +
-                                   head * a.r_head[i] + lane * 8) = out[i];
+            store_once((typename T::piece *)((typename T::elem *)a.rows[i] + token * a.r_token[i] +
+                                             head * a.r_head[i] + lane * 8), out[i]);
     }
 }
 

@@ -191,6 +191,29 @@ __device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b)
                                                                   __builtin_bit_cast(u16x2, b)));
 }
 
+// A piece past the caches' usual order: for data that is not used again soon.
+template <class P>
+__device__ __forceinline__ P load_once(const P *p)
+{
+    return __builtin_nontemporal_load(p);
+}
+__device__ __forceinline__ Fp32::piece load_once(const Fp32::piece *p)
+{
+    Fp32::piece r;
+    r.lo = __builtin_nontemporal_load(&p->lo);
+    r.hi = __builtin_nontemporal_load(&p->hi);
+    return r;
+}
+__device__ __forceinline__ void store_once(u32x4 *to, u32x4 p)
+{
+    __builtin_nontemporal_store(p, to);
+}
+__device__ __forceinline__ void store_once(Fp32::piece *to, const Fp32::piece &p)
+{
+    __builtin_nontemporal_store(p.lo, &to->lo);
+    __builtin_nontemporal_store(p.hi, &to->hi);
+}
+
 __device__ __forceinline__ void set_status(uint32_t *status, uint32_t bit)
 {
     if (status)
