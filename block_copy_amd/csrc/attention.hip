@@ -1271,8 +1271,10 @@ hipError_t attention_type(const AttentionArgs &a, const AttentionShape &shape, u
 // 155), of at least 512 keys each; a call too small for that takes splits of
 // one step of a workgroup, for the shortest chain of reads.
 // Many rows: one workgroup to a CU (two splits for each CU's workgroup of 2048
-// of 18432 cost 60 us in writing and joining them).  Tiles are counted from all
-// rows, not from the longest sequence's.
+// of 18432 cost 60 us in writing and joining them), down to splits of one tile:
+// 4 chunks of 160 over 963, 8 + 8 heads of 128, take 40 us unsplit, 27 in
+// splits of 256 keys at least, 22 of 64.  Tiles are counted from all rows, not
+// from the longest sequence's.
 AttentionShape attention_shape(uint32_t num_seqs, uint32_t total_q, uint32_t q_heads, uint32_t kv_heads,
                                uint32_t head_dim, uint32_t max_q_len, uint32_t max_context,
                                uint32_t window)
@@ -1299,8 +1301,8 @@ AttentionShape attention_shape(uint32_t num_seqs, uint32_t total_q, uint32_t q_h
         const uint64_t quick = 256 / blocks < range / unit ? 256 / blocks : range / unit;
         splits = splits > quick ? splits : quick;
     } else {
-        unit = 128;
-        splits = 256 / blocks < range / 512 ? 256 / blocks : range / 512;
+        unit = 64;   // a tile
+        splits = 256 / blocks < range / unit ? 256 / blocks : range / unit;
     }
     splits = splits < kMaxSplits ? splits : kMaxSplits;
     splits = splits ? splits : 1;
