@@ -1267,8 +1267,9 @@ hipError_t attention_type(const AttentionArgs &a, const AttentionShape &shape, u
 // workgroups than the GPU holds, the keys are split.
 //
 // Few rows: the GPU holds 512 workgroups, and ragged sequences want several
-// times that (12 x 40001 e4m3: 512 workgroups 281 us, 1024 177, 2048 153, 4096
-// 155), of at least 512 keys each; a call too small for that takes splits of
+// times that, of at least 512 keys each (12 x 40001 e4m3, before its values
+// passed the caches by: 156 us with at most 1,280 workgroups, 151 with 2,048,
+// 157 with 4,096, 173 with 6,144); a call too small for that takes splits of
 // one step of a workgroup, for the shortest chain of reads.
 // Many rows: one workgroup to a CU (two splits for each CU's workgroup of 2048
 // of 18432 cost 60 us in writing and joining them), down to splits of one tile:

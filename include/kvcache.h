@@ -194,9 +194,9 @@ int kvcache_read(const kvcache_pages_t *pages, uint32_t dtype, const kvcache_row
  *
  * max_q_len and max_context bound the lengths (they shape the launch; a longer
  * sequence sets KVCACHE_BAD_LENGTH, and what lies beyond the bound is neither
- * computed nor seen; rows of out that no sequence covers are undefined).  The workspace, kvcache_attention_workspace_bytes of the
- * same structures (it depends on the sizes alone, and may be 0), is scratch
- * for one call at a time.
+ * computed nor seen; rows of out that no sequence covers are undefined).  The
+ * workspace, kvcache_attention_workspace_bytes of the same structures (it
+ * depends on the sizes alone, and may be 0), is scratch for one call at a time.
  * errors: KVCOPY_EINVAL (struct_size; dtype not BF16 or FP16, or 16-bit pages
  * of another dtype; NULL pointers; head_dim 0 or above
  * KVCACHE_MAX_ATTENTION_HEAD_DIM; q_heads no multiple of kv_heads or above
