@@ -267,20 +267,23 @@ def read(cache: PagedCache, slots, k_out=None, v_out=None, *, dtype=None, status
 
 
 class AttentionPlan:
-    """Attention of new tokens over a cache (see kvcache_attention), for up to
+    """Attention of new tokens over a cache (see kvcache_attention), for
     num_seqs sequences and total_q new tokens: the sizes and the workspace that
     calls of one shape share.  A plan serves one call at a time; calls on
     different streams need plans of their own.
 
     scale defaults to 1 / sqrt(head_dim); window 0 means none.  num_seqs and
-    total_q are exact; max_q_len and max_context are bounds."""
+    total_q are exact; max_q_len and max_context are bounds.  dtype is the
+    queries' and the output's: the pages' own, or over 8-bit pages bfloat16 or
+    float16, by default whichever the queries of a call have."""
 
     def __init__(self, cache: PagedCache, *, q_heads: int, num_seqs: int, total_q: int, max_q_len: int,
                  max_context: int, window: int = 0, scale=None, dtype=None):
         self.cache = cache
-        self.dtype = dtype if dtype is not None else torch.bfloat16 if cache.coded else cache.dtype
-        _require(self.dtype in (torch.bfloat16, torch.float16), "rows are bfloat16 or float16")
-        a = AttentionArgs(ctypes.sizeof(AttentionArgs), _TYPES[self.dtype])
+        # None: either type, as the queries come (the workspace is the same)
+        self.dtype = dtype if dtype is not None else None if cache.coded else cache.dtype
+        _require(self.dtype in (None, *_ROW_TYPES[:2]), "rows are bfloat16 or float16")
+        a = AttentionArgs(ctypes.sizeof(AttentionArgs), _TYPES[self.dtype or torch.bfloat16])
         a.num_seqs, a.q_heads, a.total_q = num_seqs, q_heads, total_q
         a.max_q_len, a.max_context, a.window = max_q_len, max_context, window
         a.scale = 1.0 / math.sqrt(cache.head_dim) if scale is None else scale
@@ -298,11 +301,16 @@ class AttentionPlan:
         """q [total_q, q_heads, head_dim]; page_table int32 [num_seqs, columns];
         q_starts int32 [num_seqs + 1]; context_lens int32 [num_seqs].  lse, if
         given, float32 [total_q, q_heads], receives the log-sums.  Returns out."""
-        a, dev = self.args, self.cache.device
+        a, dev, dt = self.args, self.cache.device, self.dtype
+        if dt is None:
+            dt = q.dtype
+            if dt not in _ROW_TYPES[:2]:
+                raise ValueError("q must be bfloat16 or float16")
+            a.dtype = _TYPES[dt]
         if out is None:
-            out = torch.empty(self.shape, dtype=self.dtype, device=dev)
-        a.q = _rows(q, self.shape, self.dtype, dev, "q")       # a tuple fills the structure
-        a.out = _rows(out, self.shape, self.dtype, dev, "out")
+            out = torch.empty(self.shape, dtype=dt, device=dev)
+        a.q = _rows(q, self.shape, dt, dev, "q")       # a tuple fills the structure
+        a.out = _rows(out, self.shape, dt, dev, "out")
         ts, st = page_table.shape, page_table.stride()
         if (page_table.dtype != torch.int32 or page_table.device != dev or len(ts) != 2 or ts[0] != self.num_seqs
                 or ts[1] < self.columns or (ts[1] > 1 and st[1] != 1)):

@@ -1,0 +1,64 @@
+"""What the torch binding of the cache operators hands to the library, seen on
+the CPU: host tensors in place of the GPU's, and a recorder in place of the
+call, so nothing is enqueued."""
+import ctypes
+import types
+
+import pytest
+import torch
+
+from block_copy_amd import kvcache as C
+
+BF, FP, F32 = torch.bfloat16, torch.float16, torch.float32
+A = 0x10000   # an address that no call gets as far as using
+
+
+def host_cache(fmt=C.INT8, dim=64, kv=2, page=16, pages=300):
+    """What AttentionPlan reads of a PagedCache."""
+    coded = fmt in (C.FP8, C.INT8)
+    p = C.Pages(ctypes.sizeof(C.Pages), fmt, A, A, A if coded else None, A if coded else None)
+    p.k_stride[:] = p.v_stride[:] = (kv * page * dim, page * dim, dim)
+    p.ks_stride[:] = p.vs_stride[:] = (kv * page, page, 1)
+    p.num_pages, p.kv_heads, p.page_size, p.head_dim = pages, kv, page, dim
+    dtype = {C.BF16: BF, C.FP16: FP, C.FP8: torch.float8_e4m3fn, C.INT8: torch.int8}[fmt]
+    return types.SimpleNamespace(pages=p, _ref=ctypes.byref(p), coded=coded, dtype=dtype, page_size=page, head_dim=dim,
+                                 kv_heads=kv, num_pages=pages, device=torch.device("cpu"))
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The types of every attention call that reaches the library."""
+    seen = []
+    monkeypatch.setattr(C, "_call", lambda fn, where, device, stream, pages, args: seen.append(args._obj.dtype))
+    return seen
+
+
+SIZES = dict(q_heads=4, num_seqs=1, total_q=2, max_q_len=2, max_context=40)
+
+
+def attend(plan, dtype, **kw):
+    q = torch.zeros(2, 4, 64, dtype=dtype)
+    return plan(q, torch.zeros(1, 3, dtype=torch.int32), torch.tensor([0, 2], dtype=torch.int32),
+                torch.tensor([40], dtype=torch.int32), **kw)
+
+
+def test_a_plan_over_codes_takes_either_type_of_rows(calls):
+    plan = C.AttentionPlan(host_cache(), **SIZES)
+    for dt in (FP, BF, FP):
+        assert attend(plan, dt).dtype == dt
+    assert calls == [C.FP16, C.BF16, C.FP16]
+    for q, out in ((F32, F32), (BF, FP)):
+        with pytest.raises(ValueError):
+            attend(plan, q, out=torch.zeros(2, 4, 64, dtype=out))
+    assert len(calls) == 3
+
+
+def test_a_plan_for_one_type_takes_that_type(calls):
+    for plan, good, bad in ((C.AttentionPlan(host_cache(), dtype=FP, **SIZES), FP, BF),
+                            (C.AttentionPlan(host_cache(C.BF16), **SIZES), BF, FP)):
+        attend(plan, good)
+        with pytest.raises(ValueError):
+            attend(plan, bad)
+    assert calls == [C.FP16, C.BF16]
+    with pytest.raises(ValueError):
+        C.AttentionPlan(host_cache(), dtype=F32, **SIZES)
