@@ -259,7 +259,7 @@ def prepare(case, seed):
         if case["op"] == "attention":
             s["plan"] = kvcache.AttentionPlan(
                 s["cache"], q_heads=case["heads"], num_seqs=case["seqs"], total_q=sum(q),
-                max_q_len=max(q), max_context=max(c), window=case["window"], dtype=s["q"].dtype)
+                max_q_len=max(q), max_context=max(c), window=case["window"])
     return s
 
 
