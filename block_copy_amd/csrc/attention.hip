@@ -365,7 +365,7 @@ kvcache_attention_tile_kernel(const AttentionArgs a)
     const uint32_t token = a.group.div(held ? row : 0), member = a.group.mod(held ? row : 0, token);
     const int32_t pos = shift + (int32_t)token;
     const int32_t see_hi = held ? (pos < hi - 1 ? pos : hi - 1) : -1;                 // last key seen
-    const int32_t see_lo = a.window > 0 ? pos - a.window + 1 : 0;
+    const int32_t see_lo = first_seen(pos, a.window);
     // a row sees key t if t - see_lo is below see_count, unsigned
     const uint32_t see_count = see_hi < see_lo ? 0 : (uint32_t)(see_hi - see_lo) + 1;
 
@@ -817,7 +817,7 @@ __global__ __launch_bounds__(64 * kSingleWaves, DP == 256 && (__is_same(F, void)
     const uint32_t token = a.group.div(held ? col : 0), member = a.group.mod(held ? col : 0, token);
     const int32_t pos = shift + (int32_t)token;
     const int32_t see_hi = held ? (pos < hi - 1 ? pos : hi - 1) : -1;
-    const int32_t see_lo = a.window > 0 ? pos - a.window + 1 : 0;
+    const int32_t see_lo = first_seen(pos, a.window);
     // a row sees key t if t - see_lo is below see_count, unsigned
     const uint32_t see_count = see_hi < see_lo ? 0 : (uint32_t)(see_hi - see_lo) + 1;
 

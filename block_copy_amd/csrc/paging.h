@@ -48,6 +48,14 @@ KVC_HD int32_t checked_slot(int64_t slot, uint32_t num_slots)
     return slot < (int64_t)num_slots ? (int32_t)slot : -2;
 }
 
+// The first key that a row at `position` may see.  No difference is taken that
+// could leave 31 bits: a window may be as large as an int32_t, and a position
+// lies before the first key where a sequence has fewer keys than rows.
+KVC_HD int32_t first_seen(int32_t position, int32_t window)
+{
+    return window > 0 && position >= window ? position - window + 1 : 0;
+}
+
 // The keys a block of query rows has to look at: rows stand at positions
 // first .. last, see keys <= their position and, with a window, > position -
 // window; the cache holds `bound` tokens.  [lo, hi) is empty if lo >= hi.
@@ -58,9 +66,7 @@ KVC_HD KeyRange key_range(int32_t first, int32_t last, int32_t window, int32_t b
 {
     KeyRange r;
     r.hi = last + 1 < bound ? last + 1 : bound;
-    r.lo = 0;
-    if (window > 0 && first - window + 1 > 0)
-        r.lo = first - window + 1;
+    r.lo = first_seen(first, window);
     return r;
 }
 

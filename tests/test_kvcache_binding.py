@@ -2,6 +2,8 @@
 the CPU: host tensors in place of the GPU's, and a recorder in place of the
 call, so nothing is enqueued."""
 import ctypes
+import os
+import subprocess
 import types
 
 import pytest
@@ -10,6 +12,7 @@ import torch
 from block_copy_amd import kvcache as C
 
 BF, FP, F32 = torch.bfloat16, torch.float16, torch.float32
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 A = 0x10000   # an address that no call gets as far as using
 
 
@@ -62,3 +65,14 @@ def test_a_plan_for_one_type_takes_that_type(calls):
     assert calls == [C.FP16, C.BF16]
     with pytest.raises(ValueError):
         C.AttentionPlan(host_cache(), dtype=F32, **SIZES)
+
+
+def test_windows_as_large_as_they_may_be(tmp_path):
+    """tests/native/window_check.cpp, under sanitizers."""
+    exe = tmp_path / "window"
+    subprocess.run(["g++", "-O1", "-g", "-std=c++17", "-fsanitize=undefined,address", "-fno-sanitize-recover=all",
+                    "-I" + os.path.join(ROOT, "block_copy_amd", "csrc"),
+                    os.path.join(ROOT, "tests", "native", "window_check.cpp"), "-o", str(exe)],
+                   check=True, capture_output=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stdout + r.stderr
