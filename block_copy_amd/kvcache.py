@@ -7,7 +7,8 @@ devices and passes addresses.  Work is enqueued on `stream` (a
 torch.cuda.Stream or a raw handle), by default torch's current stream of the
 tensors' device.  As with any call on another stream, a tensor used on a stream
 other than the one it was made on has to be kept until that work is done
-(Tensor.record_stream, or an event).
+(Tensor.record_stream, or an event).  What a call makes itself (outputs that are
+not given, a plan's workspace) is made for the stream it works on.
 """
 from __future__ import annotations
 
@@ -116,13 +117,32 @@ def _require(ok: bool, what: str) -> None:
 _raw_stream = torch._C._cuda_getCurrentRawStream   # a tenth of the cost of torch.cuda.current_stream
 
 
+def _handle(stream, index) -> int:
+    if stream is None:
+        return _raw_stream(index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A new tensor that work on `stream` may write at once.  The allocator
+    orders the uses of a block only by the stream it was made under: one made
+    under another stream may still be written by work that is queued there."""
+    if stream is None or _handle(stream, device.index) == _raw_stream(device.index):
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else \
+            torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        out = torch.empty(shape, dtype=dtype, device=device)
+    # the caller, who waits for `stream`, goes on with it on the current one
+    out.record_stream(torch.cuda.current_stream(device))
+    return out
+
+
 def _call(fn, where: str, device, stream, *args) -> None:
     """fn(*args, stream) with `device` current."""
     index = device.index
-    if stream is None:
-        handle = _raw_stream(index)
-    else:
-        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    handle = _handle(stream, index)
     if torch.cuda.current_device() == index:
         rc = fn(*args, handle)
     else:
@@ -181,14 +201,14 @@ def rope(positions, freqs, q, k=None, *, q_out=None, k_out=None, interleaved: bo
     tokens, heads, dim = shape
     pairs = freqs.shape[0]
     if q_out is None:
-        q_out = torch.empty(shape, dtype=dt, device=dev)
+        q_out = _empty(shape, dt, dev, stream)
     k_heads, k_rows, k_out_rows = 0, _NO_ROWS, _NO_ROWS
     if k is not None:
         kshape = k.shape
         if len(kshape) != 3 or kshape[0] != tokens or kshape[2] != dim:
             raise ValueError("k must be [tokens, heads, head_dim], with q's tokens and head_dim")
         if k_out is None:
-            k_out = torch.empty(kshape, dtype=dt, device=dev)
+            k_out = _empty(kshape, dt, dev, stream)
         k_heads = kshape[1]
         k_rows, k_out_rows = _rows(k, kshape, dt, dev, "k"), _rows(k_out, kshape, dt, dev, "k_out")
     elif k_out is not None:
@@ -257,9 +277,9 @@ def read(cache: PagedCache, slots, k_out=None, v_out=None, *, dtype=None, status
     if dtype not in _ROW_TYPES:
         raise ValueError("rows are bfloat16, float16 or float32")
     if k_out is None:
-        k_out = torch.empty(shape, dtype=dtype, device=dev)
+        k_out = _empty(shape, dtype, dev, stream)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=dtype, device=dev)
+        v_out = _empty(shape, dtype, dev, stream)
     r, w = Rows(*_rows(k_out, shape, dtype, dev, "k_out")), Rows(*_rows(v_out, shape, dtype, dev, "v_out"))
     _call(lib.kvcache_read, "kvcache_read", dev, stream, cache._ref, _TYPES[dtype], ctypes.byref(r),
           ctypes.byref(w), _vector(slots, torch.int64, shape[0], dev, "slots"), shape[0], _status(status, dev))
@@ -269,8 +289,10 @@ def read(cache: PagedCache, slots, k_out=None, v_out=None, *, dtype=None, status
 class AttentionPlan:
     """Attention of new tokens over a cache (see kvcache_attention), for
     num_seqs sequences and total_q new tokens: the sizes and the workspace that
-    calls of one shape share.  A plan serves one call at a time; calls on
-    different streams need plans of their own.
+    calls of one shape share.  One thread at a time calls a plan.  It keeps a
+    workspace for each stream that it was called on, so that calls on several
+    streams do not meet; graphs captured from one plan on one stream share it,
+    need the plan kept, and must not be replayed at the same time.
 
     scale defaults to 1 / sqrt(head_dim); window 0 means none.  num_seqs and
     total_q are exact; max_q_len and max_context are bounds.  dtype is the
@@ -290,12 +312,18 @@ class AttentionPlan:
         # columns are checked against the table of each call
         a.table_columns = -(-max_context // cache.page_size)
         self.columns = a.table_columns
-        probe = lib.kvcache_attention_workspace_bytes(cache._ref, ctypes.byref(a))
-        self.workspace = torch.empty(probe, dtype=torch.uint8, device=cache.device) if probe else None
-        if probe:
-            a.workspace, a.workspace_bytes = self.workspace.data_ptr(), probe
         self.args, self._ref = a, ctypes.byref(a)
         self.shape, self.num_seqs = (total_q, q_heads, cache.head_dim), num_seqs
+        a.workspace_bytes = lib.kvcache_attention_workspace_bytes(cache._ref, ctypes.byref(a))
+        # by stream: memory made under one may be handed on while another still uses it
+        self._workspaces = {}
+        self.workspace = self._workspace(None, cache.device) if a.workspace_bytes else None   # the current stream's
+
+    def _workspace(self, stream, device):
+        handle = _handle(stream, device.index)
+        if handle not in self._workspaces:
+            self._workspaces[handle] = _empty((self.args.workspace_bytes,), torch.uint8, device, stream)
+        return self._workspaces[handle]
 
     def __call__(self, q, page_table, q_starts, context_lens, *, out=None, lse=None, status=None, stream=None):
         """q [total_q, q_heads, head_dim]; page_table int32 [num_seqs, columns];
@@ -308,7 +336,7 @@ class AttentionPlan:
                 raise ValueError("q must be bfloat16 or float16")
             a.dtype = _TYPES[dt]
         if out is None:
-            out = torch.empty(self.shape, dtype=dt, device=dev)
+            out = _empty(self.shape, dt, dev, stream)
         a.q = _rows(q, self.shape, dt, dev, "q")       # a tuple fills the structure
         a.out = _rows(out, self.shape, dt, dev, "out")
         ts, st = page_table.shape, page_table.stride()
@@ -327,5 +355,7 @@ class AttentionPlan:
         else:
             a.lse = None
         a.status = _status(status, dev)
+        if a.workspace_bytes:
+            a.workspace = self._workspace(stream, dev).data_ptr()
         _call(lib.kvcache_attention, "kvcache_attention", dev, stream, self.cache._ref, self._ref)
         return out

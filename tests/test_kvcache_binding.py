@@ -67,6 +67,32 @@ def test_a_plan_for_one_type_takes_that_type(calls):
         C.AttentionPlan(host_cache(), dtype=F32, **SIZES)
 
 
+def test_a_plan_has_a_workspace_for_each_stream(monkeypatch):
+    """Memory made under one stream is never given to a call on another."""
+    current, spaces, made = [7], [], []
+    monkeypatch.setattr(C, "_raw_stream", lambda index: current[0])
+    monkeypatch.setattr(C, "_call", lambda fn, where, device, stream, pages, args: spaces.append(args._obj.workspace))
+    empty = C._empty
+    monkeypatch.setattr(C, "_empty", lambda shape, dtype, device, stream: (
+        made.append((C._handle(stream, None), tuple(shape))), empty(shape, dtype, device, None))[1])
+    plan = C.AttentionPlan(host_cache(), **dict(SIZES, max_context=4000))
+    need = plan.args.workspace_bytes
+    assert need > 0 and made == [(7, (need,))]
+
+    def attend(stream):
+        plan(torch.zeros(2, 4, 64, dtype=BF), torch.zeros(1, 250, dtype=torch.int32),
+             torch.tensor([0, 2], dtype=torch.int32), torch.tensor([4000], dtype=torch.int32), stream=stream)
+
+    attend(None), attend(7), attend(9)
+    current[0] = 9
+    attend(None), attend(7)
+    assert spaces[0] == spaces[1] == spaces[4] == plan.workspace.data_ptr()
+    assert spaces[2] == spaces[3] != spaces[0]
+    assert [m for m in made if m[1] == (need,)] == [(7, (need,)), (9, (need,))]
+    # outputs that are not given are made for the stream that writes them
+    assert [m[0] for m in made if m[1] != (need,)] == [7, 7, 9, 9, 7]
+
+
 def test_windows_as_large_as_they_may_be(tmp_path):
     """tests/native/window_check.cpp, under sanitizers."""
     exe = tmp_path / "window"
