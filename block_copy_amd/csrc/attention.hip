@@ -1183,8 +1183,8 @@ __global__ __launch_bounds__(kJoinThreads) void kvcache_attention_join_kernel(co
 #pragma unroll
     for (int w = 0; w < kJoinThreads / 64; ++w)
         top = __builtin_fmaxf(top, wave_m[w]);
-    const float f = l == 0.0f ? 0.0f : m == top ? 1.0f : __builtin_amdgcn_exp2f(m - top);
-    weight[tid] = f;
+    const float f = m == top ? 1.0f : __builtin_amdgcn_exp2f(m - top);
+    weight[tid] = l == 0.0f ? -1.0f : f;   // not written
     l = l == 0.0f ? 0.0f : l * f;
     for (int x = 1; x < 64; x <<= 1)
         l += __shfl_xor(l, x, 64);
@@ -1202,9 +1202,9 @@ __global__ __launch_bounds__(kJoinThreads) void kvcache_attention_join_kernel(co
     if (first < at_once) {
 #pragma unroll 4
         for (uint32_t s = first; s < a.splits; s += at_once) {
-            // a weight of 0 is a split that may not have been written
+            // a weight of 0 counts: it does not hide an infinity or a NaN
             const float w = weight[s];
-            if (w != 0.0f)
+            if (w >= 0.0f)
                 y += *(const f32x4 *)(a.part_o + (s * rows + row) * a.head_dim + quad * 4) * w;
         }
     }

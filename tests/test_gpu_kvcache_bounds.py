@@ -25,3 +25,33 @@ def test_the_largest_windows_hide_nothing(C, window, q_lens, ctx, heads):
     b = base._attend(C, torch.Generator().manual_seed(3), **dict(c, window=window))
     base._compare(a, **c)
     assert base._eq_bits(a["out"], b["out"]) and torch.equal(a["lse"], b["lse"])
+
+
+@pytest.mark.parametrize("kind", [BF, FP, F8, I8])
+@pytest.mark.parametrize("q_len", [1, 40])
+@pytest.mark.parametrize("ctx", [400, 6000])
+def test_values_of_no_weight_that_read_as_nan(C, q_len, kind, ctx):
+    """A NaN that a row sees reaches it where another key takes all the weight
+    too, whichever splits the two lie in: few splits and many."""
+    page, group = 16, 4
+
+    def spoil(kp, vp, table, ks, vs):
+        a, b = int(table[0][1]), int(table[0][(ctx - q_len) // page - 1])
+        if ks is not None:
+            ks[b, :, 3] = 1e4
+            vs[a, :, 5] = math.nan
+        else:
+            kp[b, :, 3] *= 1e3
+            vp[a, :, 5] = math.nan
+    c = base._case(q_lens=[q_len], ctx=[ctx], heads=group, kv=1, dim=64, page=page, dtype=FP if kind == FP else BF,
+                   kind=kind)
+    r = base._attend(C, torch.Generator().manual_seed(5), edit=spoil, q_scale=20.0, **c)
+    assert r["out"].isnan().all()
+    splits = r["plan"].args.workspace_bytes // (q_len * group * (64 + 2) * 4)
+    assert (splits > 8) == (ctx == 6000)
+    # and an infinity does not leave as a number
+    if kind in (BF, FP):
+        def spoil_more(kp, vp, table, ks, vs):
+            spoil(kp, vp, table, ks, vs)
+            vp[int(table[0][1]), :, 5] = math.inf
+        assert not base._attend(C, torch.Generator().manual_seed(5), edit=spoil_more, q_scale=20.0, **c)["out"].isfinite().any()
