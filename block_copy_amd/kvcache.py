@@ -256,7 +256,8 @@ class PagedCache:
 
 def write(cache: PagedCache, k, v, slots, *, status=None, stream=None) -> None:
     """Writes k and v, [tokens, kv_heads, head_dim], to slots (int64 [tokens];
-    negative: left out) of the cache (see kvcache_write)."""
+    negative: left out) of the cache (see kvcache_write).  A slot that is named
+    twice ends with a mixture of both tokens."""
     if k.dim() != 3 or k.dtype not in _ROW_TYPES[:2]:
         raise ValueError("k must be a 3-dimensional bfloat16 or float16 tensor")
     dev, shape = cache.device, (k.shape[0], cache.kv_heads, cache.head_dim)

@@ -140,8 +140,11 @@ int kvcache_rope(const kvcache_rope_t *args, hipStream_t stream);
 
 /*
  * kvcache_write -- writes row t of k and v (kv_heads heads each) to slot
- * slots[t] = page * page_size + place.  A negative slot leaves the token out;
- * of two tokens with the same slot, either may be kept.  16-bit pages have
+ * slots[t] = page * page_size + place.  A negative slot leaves the token out.
+ * No two tokens of a call may share a slot of 0 or more whose contents matter:
+ * tokens are written in no order and a row in several stores, so that slot ends
+ * with codes, scales, keys and values of either, mixed (no other slot is
+ * affected; padding may go to one slot that nobody reads).  16-bit pages have
  * the rows' dtype and take them unchanged.  8-bit pages get, for each token
  * and head of k and of v, with amax the largest magnitude and Q = 448 (FP8) or
  * 127 (INT8),

@@ -55,3 +55,23 @@ def test_values_of_no_weight_that_read_as_nan(C, q_len, kind, ctx):
             spoil(kp, vp, table, ks, vs)
             vp[int(table[0][1]), :, 5] = math.inf
         assert not base._attend(C, torch.Generator().manual_seed(5), edit=spoil_more, q_scale=20.0, **c)["out"].isfinite().any()
+
+
+@pytest.mark.parametrize("dim", [128, 12])
+@pytest.mark.parametrize("kind", [BF, F8, I8])
+def test_slots_named_twice_spoil_no_other(C, kind, dim):
+    """Padding tokens that share a slot: what the others wrote is as without."""
+    g = torch.Generator().manual_seed(3)
+    tokens, heads, page = 200, 2, 16
+    k, v = (torch.randn(tokens, heads, dim, generator=g).to(BF).to(DEV) for _ in range(2))
+    slots = torch.randperm(20 * page, generator=g)[:tokens]
+    slots[slots == 0] = 20 * page       # slot 0 is the padding's
+    slots[::3] = 0
+    alone = torch.where(slots == 0, -1, slots)
+    rows = []
+    for s in (slots, alone):
+        (kp, ks, kraw), (vp, vs, vraw) = (base._blank(21, heads, page, dim, kind, "hnd", 4) for _ in range(2))
+        C.write(C.PagedCache(kp, vp, ks, vs), k, v, s.to(DEV))
+        rows.append([x.reshape(21, heads, page, -1).transpose(1, 2).flatten(0, 1)[1:]
+                     for x in (kraw, vraw, ks, vs) if x is not None])
+    assert all(base._eq_bits(a, b) for a, b in zip(*rows))
