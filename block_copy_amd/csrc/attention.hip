@@ -3,7 +3,10 @@
 //   out = sum_j p_j v_j / sum_j p_j,   p_j = exp2(c q . k_j - m),   c = scale * log2(e)
 //
 // in one pass over the keys: a running maximum m and sum of each row, and the
-// rows of the output rescaled when m has grown by more than 2^kSlack.
+// rows of the output rescaled when m has grown by more than 2^kSlack.  Weights
+// that are rounded to fp16, whose steps end at 2^-24, are kept 2^kLift larger (m
+// lies that far below the maximum): at most 2^15, so none overflows, and the
+// fixed steps begin at 2^-21 of the largest weight and are 2^-31 of it.
 //
 // Rows.  The query heads of one key/value head see the same keys, so a row is
 // a (token, query head) pair, r = token * group + head: a tile of rows reads
@@ -36,6 +39,8 @@ namespace kvc {
 namespace {
 
 constexpr float kSlack = 8.0f;
+template <class V>   // the type that weights are rounded to
+constexpr float kLift = __is_same(V, Fp16) ? 7.0f : 0.0f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kSingleWaves = 4;   // of the kernel for few rows: each its own keys
 constexpr int kSingleRows = 16;
@@ -629,8 +634,8 @@ kvcache_attention_tile_kernel(const AttentionArgs a)
                 for (int j = 0; j < 16; ++j)
                     top = __builtin_fmaxf(top, s[b][j]);
             top = __builtin_fmaxf(top, other_half(top)) * a.scale_log2;
-            if (__builtin_amdgcn_ballot_w64(top > m + kSlack)) {
-                const float grown = __builtin_fmaxf(m, top);
+            if (__builtin_amdgcn_ballot_w64(top > m + (kLift<V> + kSlack))) {
+                const float grown = __builtin_fmaxf(m, top - kLift<V>);
                 const float shrink = m == grown ? 1.0f : __builtin_amdgcn_exp2f(m - grown);
                 m = grown;
                 l *= shrink;
@@ -973,8 +978,8 @@ __global__ __launch_bounds__(64 * kSingleWaves, DP == 256 && (__is_same(F, void)
                     top = __builtin_fmaxf(top, s[b][j]);
             top = __builtin_fmaxf(top, other_half(top));
             top = __builtin_fmaxf(top, __shfl_xor(top, 16, 64)) * a.scale_log2;
-            if (__builtin_amdgcn_ballot_w64(top > m + kSlack)) {
-                const float grown = __builtin_fmaxf(m, top);
+            if (__builtin_amdgcn_ballot_w64(top > m + (kLift<V> + kSlack))) {
+                const float grown = __builtin_fmaxf(m, top - kLift<V>);
                 const float shrink = m == grown ? 1.0f : __builtin_amdgcn_exp2f(m - grown);
                 m = grown;
                 l *= shrink;
