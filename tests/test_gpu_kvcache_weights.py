@@ -64,6 +64,43 @@ def crafted(C, q_len, dtype, kind, keys, values, key_scales=None, value_scales=N
     return dict(q=q, kp=kp, vp=vp, ks=ks, vs=vs, table=table), case, out.cpu().double()
 
 
+def farthest(held):
+    """Of exp(x / 8), x a negative bfloat16 value: the x whose weight lies
+    farthest, relative to itself, from `held`'s nearest value, and that value."""
+    x = -torch.arange(64, 512, dtype=torch.float64) / 128      # 8 bits at most, scores -0.06 .. -0.5
+    x = x[x.to(BF).double() == x]
+    w = (x * DIM ** -0.5).exp()
+    off = (w.to(held).double() - w).abs() / w
+    i = int(off.argmax())
+    assert off[i] > 0.4 * R.UNIT[held]
+    return x[i].item(), w[i].to(held).item()
+
+
+@pytest.mark.parametrize("dtype,kind,q_len,unit", [
+    (BF, BF, 1, 2.0 ** -16), (BF, F8, 1, 2.0 ** -16), (BF, I8, 4, 2.0 ** -16), (FP, F8, 1, 2.0 ** -16),
+    (FP, I8, 1, 2.0 ** -16),
+    (FP, F8, 40, 2.0 ** -16), (FP, I8, 40, 2.0 ** -16)])
+def test_weights_in_two_parts(C, dtype, kind, q_len, unit):
+    """Half the keys have weight 1 and a value equal to the other keys' weight
+    rounded once, those have value -1: weights of one part give a sum of 0 where
+    it is their rounding."""
+    ctx = 150
+    x, near = farthest(FP if kind == FP else BF)
+    other = torch.arange(ctx) % 2 == 1
+    one = torch.ones(ctx, dtype=torch.float64)
+    if kind in (F8, I8):
+        r, c, got = crafted(C, q_len, dtype, kind, torch.where(other, -1.0, 0.0).double(), torch.where(other, -one, one),
+                            torch.where(other, -x * one, one), torch.where(other, one, near * one))
+    else:
+        r, c, got = crafted(C, q_len, dtype, kind, torch.where(other, x * one, 0.0 * one),
+                            torch.where(other, -one, near * one))
+    want, tol = bounds(r, c, unit)
+    assert ((got - want).abs() <= tol).all(), ((got - want).abs() / tol).max()
+    # and one part would not do
+    rounded = want + (near - math.exp(x * DIM ** -0.5)) * other.sum() / (ctx / 2 * (1 + near)) * -1
+    assert ((rounded - want).abs() > 2 * tol)[-1].all()
+
+
 @pytest.mark.parametrize("q_len", [1, 40])
 @pytest.mark.parametrize("ctx", [200, 3000])
 def test_small_weights_over_float16_pages(C, q_len, ctx):
