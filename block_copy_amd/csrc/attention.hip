@@ -287,6 +287,12 @@ __device__ __forceinline__ void store4(typename T::elem *out, const float *x)
 // (stride = 16 bytes mod 256) nor the transposing reads of V (64 mod 256) meet
 // in a bank (SQ_LDS_BANK_CONFLICT is 0).
 //
+// Weights go into the second product rounded once, to 8 bits in bf16 and 11 in
+// fp16, and their sum unrounded: over many keys the roundings cancel, and the
+// result's relative error is 0.0023 in bf16 where its own rounding alone gives
+// 0.0017 (0.00029 and 0.00021 in fp16).  A second part as in the kernel for few
+// rows is half the products again: 828 us for the chunk below.
+//
 // A chunk of 2048 tokens over 18,432, 32 + 8 heads of 128, bf16: 600 us, 970
 // TFLOP/s, where a large bf16 product reaches 1,340.  Bound by the products'
 // phase: of its 2,200 cycles 1,024 are products, the rest the first operands'
@@ -758,9 +764,9 @@ kvcache_attention_tile_kernel(const AttentionArgs a)
 // reaches 96%, 12 x 40001 in e4m3 86%: there the lookups of lines weigh more,
 // two for each half-read line of K, and the joining of the splits (5 us).
 //
-// The second product has time to spare: where it takes bf16, a weight goes in
-// as its rounding and the rest (two products), so the weights keep 16 bits.  A
-// rest of 0 or of the other sign would turn an infinite value into NaN, so
+// The second product has time to spare: a weight goes in as its rounding and
+// the rest (two products), so the weights keep 16 bits in bf16 and 22 in fp16.
+// A rest of 0 or of the other sign would turn an infinite value into NaN, so
 // these are taken out here wherever they are.
 
 template <class H, int DP>
@@ -789,7 +795,6 @@ __global__ __launch_bounds__(64 * kSingleWaves, DP == 256 && (__is_same(F, void)
     typedef std::conditional_t<kWide, u32x4, typename H::piece> Piece;
     constexpr int kPieces = DP / (8 * kPieceEights);   // of a row
     constexpr int kRowsAtOnce = 64 / kPieces, kPasses = S::kKeys / kRowsAtOnce;
-    constexpr bool kTwice = __is_same(V, Bf16);
     __shared__ __align__(16) uint8_t lds[S::kBytes];
     __shared__ float join_m[kSingleWaves][kSingleRows], join_l[kSingleWaves][kSingleRows];
 
@@ -940,7 +945,7 @@ __global__ __launch_bounds__(64 * kSingleWaves, DP == 256 && (__is_same(F, void)
 #pragma unroll
             for (int i = 0; i < kEights; ++i)
                 values[i] = value_of(i / kPieceEights, i % kPieceEights);
-            if (!H::coded && kTwice)
+            if (!H::coded)
                 special = __builtin_amdgcn_ballot_w64(any_special<V, kEights>(values)) != 0;
             if (special || edge) {
                 special = false;
@@ -1008,14 +1013,12 @@ __global__ __launch_bounds__(64 * kSingleWaves, DP == 256 && (__is_same(F, void)
                     }
                 }
                 p[i] = __builtin_bit_cast(typename V::eight, pack8<V>(w));
-                if (kTwice) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float r = w[j] - (float)p[i][j];
-                        w[j] = __builtin_isfinite(w[j]) ? r : 0.0f;
-                    }
-                    rest[i] = __builtin_bit_cast(typename V::eight, pack8<V>(w));
+                for (int j = 0; j < 8; ++j) {
+                    const float r = w[j] - (float)p[i][j];
+                    w[j] = __builtin_isfinite(w[j]) ? r : 0.0f;
                 }
+                rest[i] = __builtin_bit_cast(typename V::eight, pack8<V>(w));
             }
 
             // keys 4 group .. + 3 and 16 + 4 group .. + 3 of a pair of blocks,
@@ -1030,8 +1033,7 @@ __global__ __launch_bounds__(64 * kSingleWaves, DP == 256 && (__is_same(F, void)
             feed.run(read_v, [&](int n, typename V::eight v) {
                 const int d = n % (DP / 16), i = n / (DP / 16);
                 o[d] = V::mfma16(v, p[i], o[d]);
-                if (kTwice)
-                    o[d] = V::mfma16(v, rest[i], o[d]);
+                o[d] = V::mfma16(v, rest[i], o[d]);
             });
             if (special) {
 #pragma unroll 1

@@ -192,8 +192,9 @@ int kvcache_read(const kvcache_pages_t *pages, uint32_t dtype, const kvcache_row
  * Products are accumulated in 32 bits.  Softmax weights, multiplied with the
  * value's scale, are rounded before the second product: to fp16 where the pages
  * are FP16 (from 2^-21 of a row's largest weight down in steps of 2^-31 of it),
- * else to bf16, or to two bf16 parts (16 bits) for at most 16 rows a key/value
- * head and for FP16 rows over 8-bit pages.  Their sum is kept unrounded.  There are no atomics: the same call gives the same bits.
+ * else to bf16.  For at most 16 rows a key/value head they are two such parts (22
+ * bits in fp16, 16 in bf16), for FP16 rows over 8-bit pages always.  Their sum is
+ * kept unrounded.  There are no atomics: the same call gives the same bits.
  *
  * max_q_len and max_context bound the lengths (they shape the launch; a longer
  * sequence sets KVCACHE_BAD_LENGTH, and what lies beyond the bound is neither

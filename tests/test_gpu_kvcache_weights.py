@@ -78,7 +78,7 @@ def farthest(held):
 
 @pytest.mark.parametrize("dtype,kind,q_len,unit", [
     (BF, BF, 1, 2.0 ** -16), (BF, F8, 1, 2.0 ** -16), (BF, I8, 4, 2.0 ** -16), (FP, F8, 1, 2.0 ** -16),
-    (FP, I8, 1, 2.0 ** -16),
+    (FP, I8, 1, 2.0 ** -16), (FP, FP, 1, 2.0 ** -22), (FP, FP, 4, 2.0 ** -22),
     (FP, F8, 40, 2.0 ** -16), (FP, I8, 40, 2.0 ** -16)])
 def test_weights_in_two_parts(C, dtype, kind, q_len, unit):
     """Half the keys have weight 1 and a value equal to the other keys' weight
