@@ -112,8 +112,8 @@ int kvcache_rope_frequencies(double *out, uint32_t rot_dim, double base, int kin
  * with (a, b) = values (i, i + rot_dim / 2), or (2 i, 2 i + 1) with
  * KVCACHE_ROPE_INTERLEAVED.  KVCACHE_ROPE_INVERSE turns the other way, which
  * is also the gradient of the forward form.  The other values are copied.
- * Angles are reduced to one turn in 64 bits; the products are in 32 bits and
- * rounded once.
+ * Angles are reduced to one turn in 64 bits, and cosines and sines of FP32 rows
+ * are taken there; the products are in 32 bits and rounded once.
  *
  * q_out may be q, and k_out k, with the same strides (in place); any other
  * overlap is undefined.  k.data NULL: only q.  freq: rot_dim / 2 doubles in

@@ -75,3 +75,29 @@ def test_slots_named_twice_spoil_no_other(C, kind, dim):
         rows.append([x.reshape(21, heads, page, -1).transpose(1, 2).flatten(0, 1)[1:]
                      for x in (kraw, vraw, ks, vs) if x is not None])
     assert all(base._eq_bits(a, b) for a, b in zip(*rows))
+
+
+@pytest.mark.parametrize("dim,rot", [(64, 64), (20, 12)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_float32_turns_keep_their_bits(C, dim, rot, interleaved):
+    """Pairs (1, 0) come out as the cosine and the sine, to the last rounding:
+    half a step (2^-24), and what an angle loses in 64 bits, of which it takes
+    four roundings (the definition's product, the frequency in turns, its
+    factor, the product)."""
+    tokens = 700
+    g = torch.Generator().manual_seed(1)
+    pos = torch.randint(-2 ** 20, 2 ** 20, (tokens,), generator=g).to(torch.int32)
+    pos[:3] = torch.tensor([0, 1, 2 ** 31 - 1])
+    freqs = C.rope_frequencies(rot)
+    x = torch.zeros(tokens, 1, dim)
+    i0 = torch.arange(0, rot, 2) if interleaved else torch.arange(rot // 2)
+    i1 = i0 + 1 if interleaved else i0 + rot // 2
+    x[..., i0] = 1.0
+    angle = pos.double()[:, None] * freqs
+    for factor in (1.0, 0.5, 1.2079441308975220):
+        f = torch.tensor(factor).double()      # as 32 bits hold it
+        y, _ = C.rope(pos.to(DEV), freqs.to(DEV), x.to(DEV), interleaved=interleaved, factor=factor)
+        y = y[:, 0].cpu().double()
+        for got, want in ((y[:, i0], angle.cos() * f), (y[:, i1], angle.sin() * f)):
+            tol = want.abs() * 2.0 ** -24 * (1 + 2.0 ** -20) + angle.abs() * 4 * 2.0 ** -53 * f + 2.0 ** -150
+            assert ((got - want).abs() <= tol).all(), ((got - want).abs() / tol).max()
