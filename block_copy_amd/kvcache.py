@@ -9,6 +9,9 @@ tensors' device.  As with any call on another stream, a tensor used on a stream
 other than the one it was made on has to be kept until that work is done
 (Tensor.record_stream, or an event).  What a call makes itself (outputs that are
 not given, a plan's workspace) is made for the stream it works on.
+
+No call records a gradient: while they are on, tensors that require one are
+refused.  That of rope is rope itself, with inverse=True.
 """
 from __future__ import annotations
 
@@ -154,6 +157,14 @@ def _call(fn, where: str, device, stream, *args) -> None:
 
 # These run on every call: messages are made only when they are raised.
 
+def _no_gradient(*tensors):
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError("a tensor requires a gradient, which this call does not record: detach it, "
+                                 "or call under torch.no_grad()")
+
+
 def _status(status, device):
     if status is None:
         return None
@@ -195,6 +206,7 @@ def rope(positions, freqs, q, k=None, *, q_out=None, k_out=None, interleaved: bo
     kvcache_rope): positions int32 [tokens], freqs float64 [rot_dim / 2].
     q_out and k_out default to new tensors and may be q and k themselves.
     Returns (q_out, k_out)."""
+    _no_gradient(q, k, q_out, k_out)
     dev, dt, shape = q.device, q.dtype, q.shape
     if len(shape) != 3 or dev.type != "cuda" or dt not in _ROW_TYPES:
         raise ValueError("q must be a [tokens, heads, head_dim] bfloat16, float16 or float32 GPU tensor")
@@ -231,6 +243,7 @@ class PagedCache:
     caller's."""
 
     def __init__(self, k, v, k_scales=None, v_scales=None):
+        _no_gradient(k, v, k_scales, v_scales)
         _require(k.dim() == 4 and k.is_cuda and k.dtype in _TYPES and k.dtype != torch.float32,
                  "pages must be 4-dimensional bfloat16, float16, float8_e4m3fn or int8 GPU tensors")
         _require(v.shape == k.shape and v.dtype == k.dtype and v.device == k.device,
@@ -258,6 +271,7 @@ def write(cache: PagedCache, k, v, slots, *, status=None, stream=None) -> None:
     """Writes k and v, [tokens, kv_heads, head_dim], to slots (int64 [tokens];
     negative: left out) of the cache (see kvcache_write).  A slot that is named
     twice ends with a mixture of both tokens."""
+    _no_gradient(k, v)
     if k.dim() != 3 or k.dtype not in _ROW_TYPES[:2]:
         raise ValueError("k must be a 3-dimensional bfloat16 or float16 tensor")
     dev, shape = cache.device, (k.shape[0], cache.kv_heads, cache.head_dim)
@@ -271,6 +285,7 @@ def read(cache: PagedCache, slots, k_out=None, v_out=None, *, dtype=None, status
     k_out and v_out, [tokens, kv_heads, head_dim] (see kvcache_read); new
     tensors of `dtype` (bfloat16, or the pages' own) where not given.
     Returns (k_out, v_out)."""
+    _no_gradient(k_out, v_out)
     dev, shape = cache.device, (slots.shape[0], cache.kv_heads, cache.head_dim)
     if dtype is None:
         given = k_out if k_out is not None else v_out
@@ -330,6 +345,7 @@ class AttentionPlan:
         """q [total_q, q_heads, head_dim]; page_table int32 [num_seqs, columns];
         q_starts int32 [num_seqs + 1]; context_lens int32 [num_seqs].  lse, if
         given, float32 [total_q, q_heads], receives the log-sums.  Returns out."""
+        _no_gradient(q, out, lse)
         a, dev, dt = self.args, self.cache.device, self.dtype
         if dt is None:
             dt = q.dtype
