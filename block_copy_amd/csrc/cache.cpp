@@ -127,6 +127,28 @@ int attention_sizes(const kvcache_pages_t *p, const kvcache_attention_t *g)
     return KVCOPY_OK;
 }
 
+// How such a call is laid out, and whether its launches fit a grid of 2^32 threads.
+int attention_layout(const kvcache_pages_t *p, const kvcache_attention_t *g, AttentionShape &shape)
+{
+    shape = attention_shape(g->num_seqs, g->total_q, g->q_heads, p->kv_heads, p->head_dim, g->max_q_len,
+                            g->max_context, (uint32_t)g->window);
+    if ((uint64_t)p->kv_heads * shape.splits * shape.tiles >= 1ull << 23)
+        return KVCOPY_EINVAL;
+    return KVCOPY_OK;
+}
+
+bool attention_aligned(const kvcache_pages_t *p)
+{
+    return p->head_dim % 8 == 0 &&
+           pieces(p->k, p->format, p->k_stride[0], p->k_stride[1], p->k_stride[2]) &&
+           pieces(p->v, p->format, p->v_stride[0], p->v_stride[1], p->v_stride[2]);
+}
+
+bool no_rows(const kvcache_attention_t *g)
+{
+    return g->num_seqs == 0 || g->total_q == 0 || g->max_q_len == 0;
+}
+
 }  // namespace
 }  // namespace kvc
 
@@ -264,24 +286,31 @@ extern "C" uint64_t kvcache_attention_workspace_bytes(const kvcache_pages_t *pag
         .workspace_bytes;
 }
 
+extern "C" int kvcache_attention_check(const kvcache_pages_t *p, const kvcache_attention_t *g)
+{
+    int rc = attention_sizes(p, g);
+    AttentionShape shape;
+    if (rc == KVCOPY_OK && !no_rows(g))
+        rc = attention_layout(p, g, shape);
+    return rc != KVCOPY_OK ? rc : attention_aligned(p) ? KVCOPY_OK : KVCOPY_EALIGN;
+}
+
 extern "C" int kvcache_attention(const kvcache_pages_t *p, const kvcache_attention_t *g, hipStream_t stream)
 {
-    const int rc = attention_sizes(p, g);
+    int rc = attention_sizes(p, g);
     if (rc != KVCOPY_OK)
         return rc;
-    if (g->num_seqs == 0 || g->total_q == 0 || g->max_q_len == 0)
+    if (no_rows(g))
         return KVCOPY_OK;
     if (!g->q.data || !g->out.data || !g->q_starts || !g->context_lens || (g->max_context && !g->page_table))
         return KVCOPY_EINVAL;
-    const AttentionShape shape = attention_shape(g->num_seqs, g->total_q, g->q_heads, p->kv_heads, p->head_dim,
-                                                 g->max_q_len, g->max_context, (uint32_t)g->window);
+    AttentionShape shape;
+    rc = attention_layout(p, g, shape);
+    if (rc != KVCOPY_OK)
+        return rc;
     if (shape.workspace_bytes > g->workspace_bytes || (shape.workspace_bytes && !g->workspace))
         return KVCOPY_EINVAL;
-    if ((uint64_t)p->kv_heads * shape.splits * shape.tiles >= 1ull << 23)
-        return KVCOPY_EINVAL;
-    if (p->head_dim % 8 ||
-        !pieces(p->k, p->format, p->k_stride[0], p->k_stride[1], p->k_stride[2]) ||
-        !pieces(p->v, p->format, p->v_stride[0], p->v_stride[1], p->v_stride[2]) ||
+    if (!attention_aligned(p) ||
         !pieces(g->q.data, g->dtype, g->q.token_stride, g->q.head_stride) ||
         !pieces(g->out.data, g->dtype, g->out.token_stride, g->out.head_stride) ||
         (shape.workspace_bytes && !aligned(g->workspace, 16)) || !aligned(g->lse, 4) || !aligned(g->status, 4) ||

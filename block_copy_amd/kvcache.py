@@ -30,7 +30,7 @@ MAX_HEAD_DIM, MAX_ATTENTION_HEAD_DIM = 512, 256
 SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
 
 EXPORTS = ("kvcache_rope_frequencies", "kvcache_rope", "kvcache_write", "kvcache_read",
-           "kvcache_attention_workspace_bytes", "kvcache_attention")
+           "kvcache_attention_workspace_bytes", "kvcache_attention_check", "kvcache_attention")
 
 _ROW_TYPES = (torch.bfloat16, torch.float16, torch.float32)
 _TYPES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32,
@@ -100,6 +100,8 @@ def _declare():
         f.argtypes = [pages, u32, rows, rows, p, u64, p, p]
     lib.kvcache_attention_workspace_bytes.restype = u64
     lib.kvcache_attention_workspace_bytes.argtypes = [pages, ctypes.POINTER(AttentionArgs)]
+    lib.kvcache_attention_check.restype = ctypes.c_int
+    lib.kvcache_attention_check.argtypes = [pages, ctypes.POINTER(AttentionArgs)]
     lib.kvcache_attention.restype = ctypes.c_int
     lib.kvcache_attention.argtypes = [pages, ctypes.POINTER(AttentionArgs), p]
 
@@ -330,6 +332,7 @@ class AttentionPlan:
         self.columns = a.table_columns
         self.args, self._ref = a, ctypes.byref(a)
         self.shape, self.num_seqs = (total_q, q_heads, cache.head_dim), num_seqs
+        _check(lib.kvcache_attention_check(cache._ref, self._ref), "kvcache_attention_check")
         a.workspace_bytes = lib.kvcache_attention_workspace_bytes(cache._ref, ctypes.byref(a))
         # by stream: memory made under one may be handed on while another still uses it
         self._workspaces = {}

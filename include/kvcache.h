@@ -231,6 +231,10 @@ typedef struct kvcache_attention {
 } kvcache_attention_t;
 uint64_t kvcache_attention_workspace_bytes(const kvcache_pages_t *pages,
                                            const kvcache_attention_t *args);
+/* Whether kvcache_attention would take these sizes and pages: its checks of
+ * everything but the other pointers, their strides and the workspace, for a
+ * caller who sets up a call before its tensors are there. */
+int kvcache_attention_check(const kvcache_pages_t *pages, const kvcache_attention_t *args);
 int kvcache_attention(const kvcache_pages_t *pages, const kvcache_attention_t *args,
                       hipStream_t stream);
 

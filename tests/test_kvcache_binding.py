@@ -127,3 +127,35 @@ def test_gradients_are_not_lost_silently(calls):
             plan(y, table, starts, lens)
     plan(y.detach(), table, starts, lens)
     assert len(calls) == 3
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q_heads=3), dict(q_heads=0), dict(window=-1), dict(num_seqs=65536), dict(num_seqs=-1), dict(total_q=-2),
+    dict(total_q=1 << 31), dict(max_q_len=1 << 31), dict(max_context=(1 << 31) - 1), dict(scale=float("nan"))])
+def test_plans_that_no_call_would_take(calls, kw):
+    """Refused when they are made, not at their first call."""
+    with pytest.raises((C.KvcopyError, ValueError, TypeError)):
+        C.AttentionPlan(host_cache(), **dict(SIZES, **kw))
+
+
+def test_plans_over_pages_that_no_call_would_take(calls):
+    with pytest.raises(C.KvcopyError) as e:
+        C.AttentionPlan(host_cache(C.BF16), dtype=FP, **SIZES)
+    assert e.value.code == C.EINVAL
+    for kw, code in ((dict(dim=60), C.EALIGN), (dict(dim=264), C.EINVAL)):
+        with pytest.raises(C.KvcopyError) as e:
+            C.AttentionPlan(host_cache(**kw), **SIZES)
+        assert e.value.code == code
+    odd = host_cache()
+    odd.pages.k = A + 4
+    with pytest.raises(C.KvcopyError) as e:
+        C.AttentionPlan(odd, **SIZES)
+    assert e.value.code == C.EALIGN
+    # empty batches are plans
+    for kw in (dict(num_seqs=0, total_q=0), dict(total_q=0), dict(max_q_len=0, total_q=0), dict(max_context=0)):
+        C.AttentionPlan(host_cache(), **dict(SIZES, **kw))
+    # and so are sizes at their limits: a launch of 2^23 workgroups is beyond the grid
+    big = dict(q_heads=16, num_seqs=1, max_q_len=(1 << 28) - 8192, total_q=(1 << 28) - 8192)
+    with pytest.raises(C.KvcopyError):
+        C.AttentionPlan(host_cache(kv=2), **dict(SIZES, **dict(big, q_heads=14)))
+    C.AttentionPlan(host_cache(kv=2), **dict(SIZES, **dict(big, max_q_len=(1 << 27) - 512, total_q=(1 << 27) - 512)))
