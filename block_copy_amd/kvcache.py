@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 import struct
 
 import torch
@@ -119,6 +120,13 @@ def _require(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
+def _whole(x, bits: int, what: str) -> int:
+    """x as a whole number of this many bits; ctypes would keep its low ones."""
+    x = operator.index(x)
+    _require(0 <= x < 1 << bits, f"{what} must be at least 0 and less than 2^{bits}")
+    return x
+
+
 _raw_stream = torch._C._cuda_getCurrentRawStream   # a tenth of the cost of torch.cuda.current_stream
 
 
@@ -195,9 +203,10 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none",
     """Radians per position of each pair, float64 (kvcache_rope_frequencies);
     scaling: "none", "linear", "base" or "parts"."""
     _require(scaling in SCALINGS, f"scaling must be one of {sorted(SCALINGS)}")
-    out = torch.empty(max(1, int(rot_dim) // 2), dtype=torch.float64)
-    _check(lib.kvcache_rope_frequencies(out.data_ptr(), int(rot_dim), float(base),
-                                        SCALINGS[scaling], float(factor), int(original),
+    rot_dim, original = _whole(int(rot_dim), 16, "rot_dim"), _whole(int(original), 32, "original")
+    out = torch.empty(max(1, rot_dim // 2), dtype=torch.float64)
+    _check(lib.kvcache_rope_frequencies(out.data_ptr(), rot_dim, float(base),
+                                        SCALINGS[scaling], float(factor), original,
                                         float(low), float(high)), "kvcache_rope_frequencies")
     return out if device is None else out.to(device)
 
@@ -324,14 +333,15 @@ class AttentionPlan:
         self.dtype = dtype if dtype is not None else None if cache.coded else cache.dtype
         _require(self.dtype in (None, *_ROW_TYPES[:2]), "rows are bfloat16 or float16")
         a = AttentionArgs(ctypes.sizeof(AttentionArgs), _TYPES[self.dtype or torch.bfloat16])
-        a.num_seqs, a.q_heads, a.total_q = num_seqs, q_heads, total_q
-        a.max_q_len, a.max_context, a.window = max_q_len, max_context, window
+        for name, value in dict(num_seqs=num_seqs, q_heads=q_heads, total_q=total_q, max_q_len=max_q_len,
+                                max_context=max_context, window=window).items():
+            setattr(a, name, _whole(value, 31 if name == "window" else 32, name))
         a.scale = 1.0 / math.sqrt(cache.head_dim) if scale is None else scale
         # columns are checked against the table of each call
-        a.table_columns = -(-max_context // cache.page_size)
+        a.table_columns = -(-a.max_context // cache.page_size)
         self.columns = a.table_columns
         self.args, self._ref = a, ctypes.byref(a)
-        self.shape, self.num_seqs = (total_q, q_heads, cache.head_dim), num_seqs
+        self.shape, self.num_seqs = (a.total_q, a.q_heads, cache.head_dim), a.num_seqs
         _check(lib.kvcache_attention_check(cache._ref, self._ref), "kvcache_attention_check")
         a.workspace_bytes = lib.kvcache_attention_workspace_bytes(cache._ref, ctypes.byref(a))
         # by stream: memory made under one may be handed on while another still uses it

@@ -131,7 +131,10 @@ def test_gradients_are_not_lost_silently(calls):
 
 @pytest.mark.parametrize("kw", [
     dict(q_heads=3), dict(q_heads=0), dict(window=-1), dict(num_seqs=65536), dict(num_seqs=-1), dict(total_q=-2),
-    dict(total_q=1 << 31), dict(max_q_len=1 << 31), dict(max_context=(1 << 31) - 1), dict(scale=float("nan"))])
+    dict(total_q=1 << 31), dict(max_q_len=1 << 31), dict(max_context=(1 << 31) - 1), dict(scale=float("nan")),
+    # values that 32 bits would take for others
+    dict(q_heads=(1 << 32) + 4), dict(num_seqs=(1 << 32) + 1), dict(total_q=(1 << 32) + 2), dict(max_q_len=(1 << 32) + 2),
+    dict(max_context=(1 << 32) + 40), dict(window=1 << 32), dict(window=1 << 31), dict(max_q_len=2.5), dict(window=1.0)])
 def test_plans_that_no_call_would_take(calls, kw):
     """Refused when they are made, not at their first call."""
     with pytest.raises((C.KvcopyError, ValueError, TypeError)):
@@ -159,3 +162,9 @@ def test_plans_over_pages_that_no_call_would_take(calls):
     with pytest.raises(C.KvcopyError):
         C.AttentionPlan(host_cache(kv=2), **dict(SIZES, **dict(big, q_heads=14)))
     C.AttentionPlan(host_cache(kv=2), **dict(SIZES, **dict(big, max_q_len=(1 << 27) - 512, total_q=(1 << 27) - 512)))
+
+
+@pytest.mark.parametrize("args", [(-8,), ((1 << 32) + 64,), (64, 1e4, "parts", 2.0, -1), (64, 1e4, "parts", 2.0, (1 << 32) + 1)])
+def test_frequencies_of_sizes_beyond_32_bits(args):
+    with pytest.raises((C.KvcopyError, ValueError)):
+        C.rope_frequencies(*args)
