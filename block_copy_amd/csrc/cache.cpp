@@ -31,6 +31,21 @@ bool pieces(const void *p, uint32_t type, int64_t s0, int64_t s1, int64_t s2 = 0
     return aligned(p, bytes) && s0 % 8 == 0 && s1 % 8 == 0 && s2 % 8 == 0;
 }
 
+// The stride of a dimension, as far as it matters: one of extent 1 is never
+// stepped over, and the stride that a slice gives it may be anything.
+int64_t step(int64_t stride, uint64_t extent)
+{
+    return extent > 1 ? stride : 0;
+}
+
+struct PageSteps {
+    int64_t page, head, place;
+    PageSteps(const kvcache_pages_t *p, const int64_t *stride)
+        : page(step(stride[0], p->num_pages)), head(step(stride[1], p->kv_heads)), place(step(stride[2], p->page_size))
+    {
+    }
+};
+
 int check_pages(const kvcache_pages_t *p, uint32_t most)
 {
     if (!p || p->struct_size != sizeof(*p))
@@ -51,6 +66,11 @@ int check_pages(const kvcache_pages_t *p, uint32_t most)
         (coded && (!aligned(p->k_scale, 4) || !aligned(p->v_scale, 4))))
         return KVCOPY_EALIGN;
     return KVCOPY_OK;
+}
+
+bool rope_pieces(const kvcache_rows_t &r, const kvcache_rope_t *g, uint32_t heads)
+{
+    return pieces(r.data, g->dtype, step(r.token_stride, g->tokens), step(r.head_stride, heads));
 }
 
 // The checks and arguments that kvcache_write and kvcache_read share.
@@ -86,8 +106,9 @@ int row_args(const kvcache_pages_t *p, uint32_t dtype, const kvcache_rows_t *k, 
         a.rows[i] = rows[i]->data;
         a.r_token[i] = rows[i]->token_stride;
         a.r_head[i] = rows[i]->head_stride;
-        wide = wide && pieces(pages[i], p->format, ps[i][0], ps[i][1], ps[i][2]) &&
-               pieces(rows[i]->data, dtype, rows[i]->token_stride, rows[i]->head_stride);
+        const PageSteps s(p, ps[i]);
+        wide = wide && pieces(pages[i], p->format, s.page, s.head, s.place) &&
+               pieces(rows[i]->data, dtype, step(rows[i]->token_stride, tokens), step(rows[i]->head_stride, p->kv_heads));
     }
     a.slots = slots;
     a.status = status;
@@ -112,12 +133,14 @@ int attention_sizes(const kvcache_pages_t *p, const kvcache_attention_t *g)
         return KVCOPY_EINVAL;
     if (g->q_heads == 0 || g->q_heads > kMaxHeads || g->q_heads % p->kv_heads != 0)
         return KVCOPY_EINVAL;
-    for (int i = 0; i < 3; i += 2) {
-        const bool coded = element_bytes(p->format) == 1;
-        if ((uint64_t)p->k_stride[i] >= 1ull << 35 || (uint64_t)p->v_stride[i] >= 1ull << 35 ||
-            (coded && ((uint64_t)p->ks_stride[i] >= 1ull << 32 || (uint64_t)p->vs_stride[i] >= 1ull << 32)))
-            return KVCOPY_EINVAL;
-    }
+    // what the kernels hold in 32 bits: pieces of 8 elements, and scales
+    const auto fits = [p](const int64_t *stride, int bits) {
+        const PageSteps s(p, stride);
+        return (uint64_t)s.page < 1ull << bits && (uint64_t)s.place < 1ull << bits;
+    };
+    if (!fits(p->k_stride, 35) || !fits(p->v_stride, 35) ||
+        (element_bytes(p->format) == 1 && (!fits(p->ks_stride, 32) || !fits(p->vs_stride, 32))))
+        return KVCOPY_EINVAL;
     const uint64_t group = g->q_heads / p->kv_heads, most = (1ull << 31) - (1ull << 16);
     if (g->num_seqs > 65535 || g->total_q * group >= most || g->max_q_len * group >= most ||
         g->max_context >= most || g->window < 0 || !(std::fabs((double)g->scale) <= 1e38))
@@ -139,9 +162,9 @@ int attention_layout(const kvcache_pages_t *p, const kvcache_attention_t *g, Att
 
 bool attention_aligned(const kvcache_pages_t *p)
 {
-    return p->head_dim % 8 == 0 &&
-           pieces(p->k, p->format, p->k_stride[0], p->k_stride[1], p->k_stride[2]) &&
-           pieces(p->v, p->format, p->v_stride[0], p->v_stride[1], p->v_stride[2]);
+    const PageSteps k(p, p->k_stride), v(p, p->v_stride);
+    return p->head_dim % 8 == 0 && pieces(p->k, p->format, k.page, k.head, k.place) &&
+           pieces(p->v, p->format, v.page, v.head, v.place);
 }
 
 bool no_rows(const kvcache_attention_t *g)
@@ -236,8 +259,8 @@ extern "C" int kvcache_rope(const kvcache_rope_t *g, hipStream_t stream)
     a.factor = g->factor;
     a.sign = g->flags & KVCACHE_ROPE_INVERSE ? -1.0f : 1.0f;
     const bool wide = g->head_dim % 8 == 0 && g->rot_dim % (a.interleaved ? 8 : 16) == 0 &&
-                      pieces(a.q, g->dtype, a.q_st, a.q_sh) && pieces(a.q_out, g->dtype, a.qo_st, a.qo_sh) &&
-                      pieces(a.k, g->dtype, a.k_st, a.k_sh) && pieces(a.k_out, g->dtype, a.ko_st, a.ko_sh);
+                      rope_pieces(g->q, g, g->q_heads) && rope_pieces(g->q_out, g, g->q_heads) &&
+                      (!has_k || (rope_pieces(g->k, g, g->k_heads) && rope_pieces(g->k_out, g, g->k_heads)));
     const hipError_t e = launch_rope(a, g->dtype, wide, stream);
     return e == hipSuccess ? KVCOPY_OK : hip_fail(e);
 }
@@ -311,8 +334,8 @@ extern "C" int kvcache_attention(const kvcache_pages_t *p, const kvcache_attenti
     if (shape.workspace_bytes > g->workspace_bytes || (shape.workspace_bytes && !g->workspace))
         return KVCOPY_EINVAL;
     if (!attention_aligned(p) ||
-        !pieces(g->q.data, g->dtype, g->q.token_stride, g->q.head_stride) ||
-        !pieces(g->out.data, g->dtype, g->out.token_stride, g->out.head_stride) ||
+        !pieces(g->q.data, g->dtype, step(g->q.token_stride, g->total_q), step(g->q.head_stride, g->q_heads)) ||
+        !pieces(g->out.data, g->dtype, step(g->out.token_stride, g->total_q), step(g->out.head_stride, g->q_heads)) ||
         (shape.workspace_bytes && !aligned(g->workspace, 16)) || !aligned(g->lse, 4) || !aligned(g->status, 4) ||
         !aligned(g->page_table, 4) || !aligned(g->q_starts, 4) || !aligned(g->context_lens, 4))
         return KVCOPY_EALIGN;
@@ -330,18 +353,19 @@ extern "C" int kvcache_attention(const kvcache_pages_t *p, const kvcache_attenti
     a.v = p->v;
     a.k_scale = p->k_scale;
     a.v_scale = p->v_scale;
-    a.k_page = (uint32_t)(p->k_stride[0] / 8);
-    a.k_head = p->k_stride[1];
-    a.k_place = (uint32_t)(p->k_stride[2] / 8);
-    a.v_page = (uint32_t)(p->v_stride[0] / 8);
-    a.v_head = p->v_stride[1];
-    a.v_place = (uint32_t)(p->v_stride[2] / 8);
-    a.ks_page = (uint32_t)p->ks_stride[0];
-    a.ks_head = p->ks_stride[1];
-    a.ks_place = (uint32_t)p->ks_stride[2];
-    a.vs_page = (uint32_t)p->vs_stride[0];
-    a.vs_head = p->vs_stride[1];
-    a.vs_place = (uint32_t)p->vs_stride[2];
+    const PageSteps k(p, p->k_stride), v(p, p->v_stride), ks(p, p->ks_stride), vs(p, p->vs_stride);
+    a.k_page = (uint32_t)(k.page / 8);
+    a.k_head = k.head;
+    a.k_place = (uint32_t)(k.place / 8);
+    a.v_page = (uint32_t)(v.page / 8);
+    a.v_head = v.head;
+    a.v_place = (uint32_t)(v.place / 8);
+    a.ks_page = (uint32_t)ks.page;
+    a.ks_head = ks.head;
+    a.ks_place = (uint32_t)ks.place;
+    a.vs_page = (uint32_t)vs.page;
+    a.vs_head = vs.head;
+    a.vs_place = (uint32_t)vs.place;
     a.table = g->page_table;
     a.table_stride = g->table_stride;
     a.q_starts = g->q_starts;
@@ -356,9 +380,8 @@ extern "C" int kvcache_attention(const kvcache_pages_t *p, const kvcache_attenti
     a.head_dim = p->head_dim;
     a.full = p->head_dim == 64 || p->head_dim == 128 || p->head_dim == 256;
     if (element_bytes(p->format) == 1)
-        for (int i = 0; i < 3; ++i)
-            a.full = a.full && aligned(p->k, 16) && aligned(p->v, 16) && p->k_stride[i] % 16 == 0 &&
-                     p->v_stride[i] % 16 == 0;
+        a.full = a.full && aligned(p->k, 16) && aligned(p->v, 16) && k.page % 16 == 0 && k.head % 16 == 0 &&
+                 k.place % 16 == 0 && v.page % 16 == 0 && v.head % 16 == 0 && v.place % 16 == 0;
     a.tiles = shape.tiles;
     a.splits = shape.splits;
     a.split_keys = shape.split_keys;

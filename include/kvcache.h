@@ -16,7 +16,8 @@
  *     no output and no workspace.
  *   - Structures start with struct_size = sizeof(the structure).
  *   - Pointers are device addresses.  Strides count elements, not bytes; the
- *     innermost dimension (head_dim) is contiguous.
+ *     innermost dimension (head_dim) is contiguous.  The stride of a dimension
+ *     of extent 1 is ignored.
  *   - What lives in device memory cannot be checked on the host: the kernels
  *     bound every page number, slot, row range and length themselves, never
  *     access memory outside the arrays described, and, if `status` is given,

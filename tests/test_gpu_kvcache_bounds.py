@@ -101,3 +101,48 @@ def test_float32_turns_keep_their_bits(C, dim, rot, interleaved):
         for got, want in ((y[:, i0], angle.cos() * f), (y[:, i1], angle.sin() * f)):
             tol = want.abs() * 2.0 ** -24 * (1 + 2.0 ** -20) + angle.abs() * 4 * 2.0 ** -53 * f + 2.0 ** -150
             assert ((got - want).abs() <= tol).all(), ((got - want).abs() / tol).max()
+
+
+@pytest.mark.parametrize("kind", [BF, I8])
+def test_strides_of_one_token_head_or_page(C, kind):
+    """One token (or head, page, place) of a tensor whose other strides are
+    odd: what a slice of a wider buffer looks like."""
+    g = torch.Generator().manual_seed(11)
+
+    def odd(x, dim):
+        """x with a stride along dim, of extent 1, that is no multiple of 8."""
+        st = list(x.stride())
+        st[dim] = 12345677
+        return x.as_strided(x.shape, st)
+
+    for tokens, heads, kv, page, ctx in ((1, 4, 2, 16, 40), (3, 1, 1, 16, 40), (1, 2, 1, 1, 5), (30, 4, 1, 64, 50)):
+        c = base._case(q_lens=[tokens], ctx=[ctx], heads=heads, kv=kv, page=page, dtype=BF, kind=kind)
+        r = base._attend(C, g, **c)
+        q, *rest = r["args"]
+        k, v, ks, vs = r["kp"], r["vp"], r["ks"], r["vs"]
+        if kv == 1:
+            k, v = odd(k, 1), odd(v, 1)
+            if ks is not None:
+                ks, vs = odd(ks, 1), odd(vs, 1)
+        if page == 1:
+            k, v = odd(k, 2), odd(v, 2)
+        if heads == 1:
+            q = odd(q, 1)
+        out = torch.zeros_like(r["out"])
+        if tokens == 1:
+            q, out = odd(q, 0), odd(out, 0)
+        cache = C.PagedCache(k, v, ks, vs)
+        plan = C.AttentionPlan(cache, q_heads=heads, num_seqs=1, total_q=tokens, max_q_len=tokens, max_context=ctx)
+        plan(q, *rest, out=out)
+        assert base._eq_bits(out, r["out"])
+        # the same rows through writes, reads and turns
+        x = torch.randn(tokens, kv, 64, generator=g).to(BF).to(DEV)
+        y = odd(x, 0) if tokens == 1 else odd(x, 1) if kv == 1 else x
+        slots = torch.randperm(k.shape[0] * page, generator=g)[:tokens].to(DEV)
+        C.write(cache, y, y, slots)
+        got = [t.clone() for t in C.read(cache, slots)]
+        plain = C.PagedCache(r["kp"], r["vp"], r["ks"], r["vs"])
+        C.write(plain, x, x, slots)
+        assert all(torch.equal(a, b) for a, b in zip(got, C.read(plain, slots)))
+        pos, freqs = torch.arange(tokens, dtype=torch.int32, device=DEV), C.rope_frequencies(64, device=DEV)
+        assert torch.equal(C.rope(pos, freqs, y)[0], C.rope(pos, freqs, x)[0])

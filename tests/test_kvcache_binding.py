@@ -168,3 +168,26 @@ def test_plans_over_pages_that_no_call_would_take(calls):
 def test_frequencies_of_sizes_beyond_32_bits(args):
     with pytest.raises((C.KvcopyError, ValueError)):
         C.rope_frequencies(*args)
+
+
+def test_strides_of_one_do_not_matter():
+    """A dimension of extent 1 is never stepped over, whatever its stride."""
+    def check(**kw):
+        pages = host_cache(C.INT8, kv=kw.get("kv_heads", 2), page=kw.get("page_size", 16), pages=kw.get("num_pages", 9)).pages
+        for n, v in kw.items():
+            if isinstance(v, dict):
+                for i, stride in v.items():
+                    getattr(pages, n)[i] = stride
+        a = C.AttentionArgs(ctypes.sizeof(C.AttentionArgs), C.BF16)
+        a.num_seqs = a.total_q = a.max_q_len = a.table_columns = 1
+        a.q_heads, a.max_context, a.scale = 2, 1, 1.0
+        return C.lib.kvcache_attention_check(ctypes.byref(pages), ctypes.byref(a))
+
+    for n, i in (("num_pages", 0), ("kv_heads", 1), ("page_size", 2)):
+        for name in ("k_stride", "v_stride"):
+            for stride in (3, -5, 1 << 50):
+                assert check(**{n: 1, name: {i: stride}}) == C.OK, (n, name, stride)
+            assert check(**{n: 2, name: {i: 3}}) == C.EALIGN
+    for name in ("ks_stride", "vs_stride"):
+        assert check(num_pages=1, **{name: {0: -7}}) == C.OK and check(page_size=1, **{name: {2: 1 << 40}}) == C.OK
+        assert check(num_pages=2, **{name: {0: -7}}) == C.EINVAL
