@@ -155,7 +155,7 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
 def _call(fn, where: str, device, stream, *args) -> None:
     """fn(*args, stream) with `device` current."""
     index = device.index
-    handle = _handle(stream, index)
+    handle = _raw_stream(index) if stream is None else _handle(stream, index)
     if torch.cuda.current_device() == index:
         rc = fn(*args, handle)
     else:
@@ -167,12 +167,11 @@ def _call(fn, where: str, device, stream, *args) -> None:
 
 # These run on every call: messages are made only when they are raised.
 
-def _no_gradient(*tensors):
-    if torch.is_grad_enabled():
-        for t in tensors:
-            if t is not None and t.requires_grad:
-                raise ValueError("a tensor requires a gradient, which this call does not record: detach it, "
-                                 "or call under torch.no_grad()")
+def _no_gradient(t):
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError("a tensor requires a gradient, which this call does not record: detach it, "
+                         "or call under torch.no_grad()")
+
 
 
 def _status(status, device):
@@ -194,6 +193,8 @@ def _rows(t, shape, dtype, device, what):
     if t.dtype != dtype or t.device != device or t.shape != shape or (st[2] != 1 and shape[2] != 1):
         raise ValueError(f"{what} must be {dtype} of shape {tuple(shape)} on {device}, "
                          "its last dimension contiguous")
+    if t.requires_grad:
+        _no_gradient(t)
     return t.data_ptr(), st[0], st[1]
 
 
@@ -217,7 +218,6 @@ def rope(positions, freqs, q, k=None, *, q_out=None, k_out=None, interleaved: bo
     kvcache_rope): positions int32 [tokens], freqs float64 [rot_dim / 2].
     q_out and k_out default to new tensors and may be q and k themselves.
     Returns (q_out, k_out)."""
-    _no_gradient(q, k, q_out, k_out)
     dev, dt, shape = q.device, q.dtype, q.shape
     if len(shape) != 3 or dev.type != "cuda" or dt not in _ROW_TYPES:
         raise ValueError("q must be a [tokens, heads, head_dim] bfloat16, float16 or float32 GPU tensor")
@@ -254,7 +254,6 @@ class PagedCache:
     caller's."""
 
     def __init__(self, k, v, k_scales=None, v_scales=None):
-        _no_gradient(k, v, k_scales, v_scales)
         _require(k.dim() == 4 and k.is_cuda and k.dtype in _TYPES and k.dtype != torch.float32,
                  "pages must be 4-dimensional bfloat16, float16, float8_e4m3fn or int8 GPU tensors")
         _require(v.shape == k.shape and v.dtype == k.dtype and v.device == k.device,
@@ -270,6 +269,8 @@ class PagedCache:
                 _require(x.shape == k.shape[:3] and x.dtype == torch.float32 and x.device == k.device,
                          "scales must be float32 of shape [num_pages, kv_heads, page_size]")
             scales = [k_scales.data_ptr(), v_scales.data_ptr(), k_scales.stride(), v_scales.stride()]
+        for x in (k, v, *((k_scales, v_scales) if coded else ())):
+            _no_gradient(x)
         p = Pages(ctypes.sizeof(Pages), _TYPES[k.dtype], k.data_ptr(), v.data_ptr(), scales[0], scales[1],
                   ks[:3], vs[:3], scales[2], scales[3], *k.shape)
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
@@ -282,7 +283,6 @@ def write(cache: PagedCache, k, v, slots, *, status=None, stream=None) -> None:
     """Writes k and v, [tokens, kv_heads, head_dim], to slots (int64 [tokens];
     negative: left out) of the cache (see kvcache_write).  A slot that is named
     twice ends with a mixture of both tokens."""
-    _no_gradient(k, v)
     if k.dim() != 3 or k.dtype not in _ROW_TYPES[:2]:
         raise ValueError("k must be a 3-dimensional bfloat16 or float16 tensor")
     dev, shape = cache.device, (k.shape[0], cache.kv_heads, cache.head_dim)
@@ -296,7 +296,6 @@ def read(cache: PagedCache, slots, k_out=None, v_out=None, *, dtype=None, status
     k_out and v_out, [tokens, kv_heads, head_dim] (see kvcache_read); new
     tensors of `dtype` (bfloat16, or the pages' own) where not given.
     Returns (k_out, v_out)."""
-    _no_gradient(k_out, v_out)
     dev, shape = cache.device, (slots.shape[0], cache.kv_heads, cache.head_dim)
     if dtype is None:
         given = k_out if k_out is not None else v_out
@@ -358,7 +357,6 @@ class AttentionPlan:
         """q [total_q, q_heads, head_dim]; page_table int32 [num_seqs, columns];
         q_starts int32 [num_seqs + 1]; context_lens int32 [num_seqs].  lse, if
         given, float32 [total_q, q_heads], receives the log-sums.  Returns out."""
-        _no_gradient(q, out, lse)
         a, dev, dt = self.args, self.cache.device, self.dtype
         if dt is None:
             dt = q.dtype
@@ -380,6 +378,7 @@ class AttentionPlan:
         if lse is not None:
             if lse.dtype != torch.float32 or lse.device != dev or lse.shape != self.shape[:2]:
                 raise ValueError(f"lse must be float32 {self.shape[:2]} on {dev}")
+            _no_gradient(lse)
             a.lse_token_stride, a.lse_head_stride = lse.stride()
             a.lse = lse.data_ptr()
         else:

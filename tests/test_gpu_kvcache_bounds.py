@@ -146,3 +146,20 @@ def test_strides_of_one_token_head_or_page(C, kind):
         assert all(torch.equal(a, b) for a, b in zip(got, C.read(plain, slots)))
         pos, freqs = torch.arange(tokens, dtype=torch.int32, device=DEV), C.rope_frequencies(64, device=DEV)
         assert torch.equal(C.rope(pos, freqs, y)[0], C.rope(pos, freqs, x)[0])
+
+
+def test_gradients_are_not_lost_silently(C):
+    """What would need one is refused while gradients are on."""
+    x = torch.ones(2, 4, 64, dtype=BF, device=DEV)
+    y = x.clone().requires_grad_()
+    pos, freqs = torch.arange(2, dtype=torch.int32, device=DEV), C.rope_frequencies(64, device=DEV)
+    p, s = torch.zeros(3, 4, 16, 64, device=DEV), torch.zeros(3, 4, 16, device=DEV)
+    for ask in (lambda: C.rope(pos, freqs, y), lambda: C.rope(pos, freqs, x, y), lambda: C.rope(pos, freqs, x, q_out=y),
+                lambda: C.rope(pos, freqs, x, x, k_out=y),
+                lambda: C.PagedCache(p.to(BF).requires_grad_(), p.to(BF)), lambda: C.PagedCache(p.to(BF), p.to(BF).requires_grad_()),
+                lambda: C.PagedCache(p.to(I8), p.to(I8), s, s.clone().requires_grad_())):
+        with pytest.raises(ValueError, match="gradient"):
+            ask()
+    with torch.no_grad():
+        a, _ = C.rope(pos, freqs, y)
+    assert torch.equal(a, C.rope(pos, freqs, x)[0]) and not a.requires_grad

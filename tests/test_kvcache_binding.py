@@ -109,15 +109,12 @@ def test_gradients_are_not_lost_silently(calls):
     x = torch.zeros(2, 4, 64, dtype=BF)
     y = x.clone().requires_grad_()
     cache, plan = host_cache(kv=4), C.AttentionPlan(host_cache(), **SIZES)
-    pos, freqs, slots = torch.zeros(2, dtype=torch.int32), torch.zeros(32, dtype=torch.float64), torch.arange(2)
+    slots = torch.arange(2)
     table, starts, lens = torch.zeros(1, 3, dtype=torch.int32), torch.tensor([0, 2], dtype=torch.int32), \
         torch.tensor([40], dtype=torch.int32)
-    asks = [lambda: C.rope(pos, freqs, y), lambda: C.rope(pos, freqs, x, y), lambda: C.rope(pos, freqs, x, q_out=y),
-            lambda: C.rope(pos, freqs, x, x, k_out=y), lambda: C.write(cache, y, x, slots),
-            lambda: C.write(cache, x, y, slots), lambda: C.read(cache, slots, y, x), lambda: C.read(cache, slots, x, y),
+    asks = [lambda: C.write(cache, y, x, slots), lambda: C.write(cache, x, y, slots), lambda: C.read(cache, slots, y, x), lambda: C.read(cache, slots, x, y),
             lambda: plan(y, table, starts, lens), lambda: plan(x, table, starts, lens, out=y),
-            lambda: plan(x, table, starts, lens, lse=torch.zeros(2, 4, requires_grad=True)),
-            lambda: C.PagedCache(torch.zeros(3, 2, 16, 64, requires_grad=True), torch.zeros(3, 2, 16, 64))]
+            lambda: plan(x, table, starts, lens, lse=torch.zeros(2, 4, requires_grad=True))]
     for ask in asks:
         with pytest.raises(ValueError, match="gradient"):
             ask()
