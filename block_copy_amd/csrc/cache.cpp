@@ -157,6 +157,9 @@ int attention_layout(const kvcache_pages_t *p, const kvcache_attention_t *g, Att
                             g->max_context, (uint32_t)g->window);
     if ((uint64_t)p->kv_heads * shape.splits * shape.tiles >= 1ull << 23)
         return KVCOPY_EINVAL;
+    // splits are joined by a workgroup of 256 for up to every row
+    if (shape.splits > 1 && (uint64_t)g->total_q * g->q_heads >= 1ull << 24)
+        return KVCOPY_EINVAL;
     return KVCOPY_OK;
 }
 

@@ -188,3 +188,23 @@ def test_strides_of_one_do_not_matter():
     for name in ("ks_stride", "vs_stride"):
         assert check(num_pages=1, **{name: {0: -7}}) == C.OK and check(page_size=1, **{name: {2: 1 << 40}}) == C.OK
         assert check(num_pages=2, **{name: {0: -7}}) == C.EINVAL
+
+
+def test_more_rows_than_the_join_of_splits_takes():
+    """Refused before the first launch, not after it."""
+    pages = host_cache().pages
+
+    def check(**kw):
+        a = C.AttentionArgs(ctypes.sizeof(C.AttentionArgs), C.BF16)
+        a.num_seqs = a.max_q_len = 1
+        a.q_heads, a.scale, a.max_context, a.table_columns = 16, 1.0, 4096, 256
+        for n, v in kw.items():
+            setattr(a, n, v)
+        return C.lib.kvcache_attention_check(ctypes.byref(pages), ctypes.byref(a)), \
+            C.lib.kvcache_attention_workspace_bytes(ctypes.byref(pages), ctypes.byref(a))
+    for n in (1, 40):
+        assert check(total_q=1 << 20, max_q_len=n)[0] == C.EINVAL
+        rc, need = check(total_q=(1 << 20) - 1, max_q_len=n)
+        assert rc == C.OK and need > 0
+        rc, need = check(total_q=1 << 20, max_q_len=n, max_context=32)      # one split: nothing is joined
+        assert rc == C.OK and need == 0
