@@ -163,3 +163,35 @@ def test_gradients_are_not_lost_silently(C):
     with torch.no_grad():
         a, _ = C.rope(pos, freqs, y)
     assert torch.equal(a, C.rope(pos, freqs, x)[0]) and not a.requires_grad
+
+
+@pytest.mark.parametrize("kind", [BF, F8])
+@pytest.mark.parametrize("q_lens,ctx", [([1, 1, 1], [500, 333, 96]), ([40, 7, 20], [500, 333, 96])])
+def test_sequences_that_share_pages(C, kind, q_lens, ctx):
+    """A common prefix, held once."""
+    def share(kp, vp, table, ks, vs):
+        table[1, :5], table[2, :6] = table[0, :5], table[0, :6]
+    c = base._case(q_lens=q_lens, ctx=ctx, heads=4, kv=2, dim=128, dtype=BF, kind=kind)
+    r = base._attend(C, torch.Generator().manual_seed(2), edit=share, **c)
+    assert len(set(r["table"][:, 0].tolist())) == 1
+    base._compare(r, **c)
+
+
+@pytest.mark.parametrize("dtype,kind", [(BF, BF), (FP, I8)])
+@pytest.mark.parametrize("q_lens,bound", [([1, 1], 1), ([1, 1], 3), ([1, 1], 300), ([3, 2], 16), ([40, 23], 700)])
+@pytest.mark.parametrize("window", [0, 50])
+def test_bounds_beyond_the_lengths(C, dtype, kind, q_lens, bound, window):
+    """max_q_len, max_context and a table for more than there is."""
+    c = base._case(q_lens=q_lens, ctx=[333, 70], heads=4, kv=2, dtype=dtype, kind=kind, window=window)
+    r = base._attend(C, torch.Generator().manual_seed(2), **c)
+    q, table, starts, lens = r["args"]
+    wide = torch.full((2, 400), -3, dtype=torch.int32, device=DEV)
+    wide[:, :table.shape[1]] = table
+    for most in (333, 334, 6400):
+        plan = C.AttentionPlan(r["cache"], q_heads=4, num_seqs=2, total_q=sum(q_lens), max_q_len=bound, max_context=most,
+                               window=window)
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        lse = torch.empty(sum(q_lens), 4, device=DEV)
+        out = plan(q, wide, starts, lens, lse=lse, status=status)
+        assert status.item() == 0
+        base._compare(dict(r, out=out, lse=lse), **c)
