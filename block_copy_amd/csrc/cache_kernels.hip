@@ -22,8 +22,8 @@ constexpr uint32_t kMaxBlocks = 1u << 22;
 // a position of 2^20 has lost 2^-4 radians in 32) costs little beside the
 // heads' traffic.  The rows are read past the caches (their last use: 64.2
 // against 66.6 us for 16,384 tokens of 32 + 8 heads of 128 in bf16, 5.2 TB/s of
-// reads and writes, where a large copy reaches 4.9); the results, used next, go
-// through them.
+// reads and writes, where the runtime's copy reaches 5.0 to 5.2 and kvcopy's
+// own, at its best shape, 6.2); the results, used next, go through them.
 
 struct Turn {
     float c, s;
